@@ -67,13 +67,16 @@ extern "C" {
 #define PKV_DEV_LAYOUT 16        /* shared-memory window misaligned (kernel skipped)  */
 #define PKV_DEV_BAD_SCALE 32     /* a per-KV-head E4M3 scale is not > 0               */
 #define PKV_DEV_BAD_ROW 64       /* a gathered row index outside its table            */
+#define PKV_DEV_BAD_TREE 128     /* a drafted token's parent does not come before it  */
 
 /* Library ABI version: PKV_ABI_VERSION of the build (incremented when an entry point is
  * added or a signature changes).  2 added paged_kv_write_fp8_per_head,
  * paged_attention_decode_fp8_per_head, pkv_pool_save and pkv_pool_load; 3 added
  * paged_decode_step, paged_decode_step_fp8 and pkv_sched_pack; 4 added
- * paged_gather_rows, pkv_step_launch and pkv_engine_step. */
-#define PKV_ABI_VERSION 4
+ * paged_gather_rows, pkv_step_launch and pkv_engine_step; 5 added the drafted-tree calls
+ * (paged_tree_masks, paged_qk_norm_rope_write, paged_attention_tree, paged_tree_commit,
+ * their _fp8 forms and paged_attention_tree_workspace_size). */
+#define PKV_ABI_VERSION 5
 int paged_kv_version(void);
 
 /* Human-readable text of a PKV_ERR_* code. Never NULL; static storage. */
@@ -322,6 +325,157 @@ int paged_attention_prefill(uint16_t *out, const uint16_t *q, const uint16_t *k_
                             int num_q_heads, int num_kv_heads, int head_dim, int block_size,
                             int num_blocks, float scale, int max_query_len, int32_t *err_flag,
                             void *stream);
+
+/* ------------------------------------------------------------------------------------
+ * Drafted trees.  A step that checks several drafted tokens per sequence at once: the
+ * drafts of a sequence form a tree (each token's parent is another draft or the cached
+ * context); they take slots of their own in the paged cache, and one pass scores them all.
+ *   1. paged_tree_masks          parents -> which drafts each one sees, and its position
+ *   2. paged_qk_norm_rope_write  head-wise norm and rotary positions of q and k; k and v
+ *                                written at the drafts' slots
+ *   3. paged_attention_tree      every draft over its cached context and its ancestors
+ *   4. paged_tree_commit         the accepted path's K/V rows moved to the slots that follow
+ *                                the context
+ * Call 2 serves any step (decode rows, prompt chunks), not only trees.  Sequence s owns the
+ * L = query_start[s+1] - query_start[s] rows from query_start[s] on (query_start: int32
+ * [num_seqs + 1], device); they are the last L of its context_lens[s] cached tokens.  Rows
+ * at or past query_start[num_seqs] are padding and left as they are.
+ * ------------------------------------------------------------------------------------ */
+#define PKV_TREE_MAX_TOKENS 1024 /* most drafts of one sequence                       */
+
+/*
+ * paged_tree_masks -- masks[row][w] bit b (row = query_start[s] + i, uint64 [num_tokens]
+ * [mask_words]) is set when tree token 64 w + b is token i or one of its ancestors;
+ * positions[row] (int32, may be NULL) = base + depth, the depth of a token under the context
+ * being 0 and base = position_base[s] (int32 [num_seqs]) or, position_base NULL,
+ * context_lens[s] - L.  parents: int32 [num_tokens], the index within the sequence's tree of
+ * each token's parent, smaller than its own, or -1 for the context; any other value sets
+ * PKV_DEV_BAD_TREE and counts as -1.  1 <= mask_words <= PKV_TREE_MAX_TOKENS / 64 (else
+ * PKV_ERR_SHAPE).  A sequence with L > 64 mask_words, L > context_lens[s] or rows outside
+ * [0, num_tokens] sets PKV_DEV_BAD_CONTEXT and its rows are left unwritten.
+ */
+int paged_tree_masks(uint64_t *masks, int32_t *positions, const int32_t *parents,
+                     const int32_t *query_start, const int32_t *context_lens,
+                     const int32_t *position_base, int num_seqs, int num_tokens, int mask_words,
+                     int32_t *err_flag, void *stream);
+
+/*
+ * paged_qk_norm_rope_write -- what stands between the q/k/v projections and attention.
+ * For every token t and head h of q (into q_out) and of k (into the cache at
+ * slot_mapping[t], as paged_kv_write):
+ *   y = x / sqrt(mean(x^2) + eps) * weight     (q_weight, k_weight: bf16 [head_dim], 16-byte
+ *                                               aligned, or NULL: no norm)
+ *   (a, b) -> rope_scale * (a cos t - b sin t, b cos t + a sin t) for each rotary pair i,
+ *   t = positions[pair_axis[i]][t] * inv_freq[i]
+ * with pairs (y[i], y[i + rotary_dim/2]), or (y[2i], y[2i+1]) with interleaved != 0;
+ * elements at or past rotary_dim pass.  v is written as it is.  Computed in fp32 and rounded
+ * once.  Angles are exact to about 2^-53 times the position (any int32 position).
+ * q, k, v, q_out: head rows of head_dim elements, heads adjacent, tokens *_stride elements
+ * apart (multiples of 8, at least the row of heads), so they may be slices of one packed
+ * projection.  q_out may be q itself (same address and stride); other overlap is not
+ * allowed.  positions: int32, axis a of token t at a * axis_stride + t (axis_stride 0: all
+ * axes share them).  num_axes 1..4.  pair_axis: HOST array of rotary_dim/2 bytes, read
+ * during the call (NULL: axis 0; an entry >= num_axes returns PKV_ERR_ARG).  inv_freq: fp64
+ * device array of rotary_dim/2 radians per position.  rotary_dim: 0 or a multiple of 16 up
+ * to head_dim; head_dim 64 or 128.  A negative slot writes no k and v (q_out is written); a
+ * slot outside the pool sets PKV_DEV_BAD_SLOT and does the same.
+ */
+int paged_qk_norm_rope_write(uint16_t *q_out, int64_t q_out_stride, const uint16_t *q,
+                             int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                             const uint16_t *v, int64_t v_stride, const uint16_t *q_weight,
+                             const uint16_t *k_weight, float eps, const int32_t *positions,
+                             int64_t axis_stride, int num_axes, const uint8_t *pair_axis,
+                             const double *inv_freq, int rotary_dim, int interleaved,
+                             float rope_scale, const int64_t *slot_mapping, int num_tokens,
+                             uint16_t *k_cache, uint16_t *v_cache, int num_blocks,
+                             int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                             int32_t *err_flag, void *stream);
+
+/* The same into E4M3 caches (layouts and codes of paged_kv_write_fp8; k's code is that of
+ * its fp32 value after the rotation).  Scales as in paged_decode_step_fp8: k_scales and
+ * v_scales both non-NULL, one per KV head (k_scale and v_scale ignored; one that is not > 0
+ * sets PKV_DEV_BAD_SCALE and skips the head's rows), or both NULL, one per cache. */
+int paged_qk_norm_rope_write_fp8(uint16_t *q_out, int64_t q_out_stride, const uint16_t *q,
+                                 int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                                 const uint16_t *v, int64_t v_stride, const uint16_t *q_weight,
+                                 const uint16_t *k_weight, float eps, const int32_t *positions,
+                                 int64_t axis_stride, int num_axes, const uint8_t *pair_axis,
+                                 const double *inv_freq, int rotary_dim, int interleaved,
+                                 float rope_scale, const int64_t *slot_mapping, int num_tokens,
+                                 uint8_t *k_cache, uint8_t *v_cache, int num_blocks,
+                                 int num_q_heads, int num_kv_heads, int head_dim,
+                                 int block_size, float k_scale, float v_scale,
+                                 const float *k_scales, const float *v_scales,
+                                 int32_t *err_flag, void *stream);
+
+/* Bytes of device workspace paged_attention_tree needs on the current device (the number of
+ * sequences and their lengths do not enter).  0 for sizes out of range. */
+size_t paged_attention_tree_workspace_size(int num_q_heads, int num_kv_heads, int head_dim,
+                                           int max_query_len);
+
+/*
+ * paged_attention_tree -- row i of sequence s attends to the context_lens[s] - L cached
+ * tokens before the tree and to tree token j (at position context_lens[s] - L + j) where bit
+ * j of its tree_masks row is set (bits at or past L are ignored; a token's own bit counts
+ * like any other):
+ *   out[row][h] = sum_t exp(x_t - max x) V_t / sum_t exp(x_t - max x),
+ *   x_t = scale * q[row][h] . K_t
+ * over those t, as paged_attention_prefill computes it (scale > 0).  A row that sees no
+ * token gives zeros.  A token that a row does not see takes no part in it, whatever its K
+ * and V rows hold.  The drafts' K/V must be in the cache.  max_query_len: host bound of
+ * every L, at most 64 mask_words.  A sequence with L > max_query_len, L > context_lens[s], a
+ * context beyond its block table or rows outside [0, num_tokens] sets PKV_DEV_BAD_CONTEXT
+ * and its rows are left unwritten; a bad block id sets PKV_DEV_BAD_BLOCK and the rows of its
+ * sequence are unspecified.  L == 1 with bit 0 is a decode row.  The key range of one
+ * sequence is split over CTAs and joined; the result does not depend on timing.
+ * workspace: as paged_attention_decode's (256-byte aligned scratch, no initialisation; calls
+ * that share one must be ordered).  head_dim 64 or 128, num_seqs <= 65535.
+ */
+int paged_attention_tree(uint16_t *out, const uint16_t *q, const uint16_t *k_cache,
+                         const uint16_t *v_cache, const int32_t *block_tables,
+                         const int32_t *context_lens, const int32_t *query_start,
+                         const uint64_t *tree_masks, int mask_words, int num_seqs,
+                         int num_tokens, int max_blocks_per_seq, int num_q_heads,
+                         int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                         float scale, int max_query_len, void *workspace,
+                         size_t workspace_bytes, int32_t *err_flag, void *stream);
+
+/* The same over E4M3 caches (q and the weights enter the products as f16, as in
+ * paged_attention_decode_fp8).  Scales as in paged_decode_step_fp8; a per-head scale that is
+ * not > 0 sets PKV_DEV_BAD_SCALE and the rows reading that head are unspecified. */
+int paged_attention_tree_fp8(uint16_t *out, const uint16_t *q, const uint8_t *k_cache,
+                             const uint8_t *v_cache, const int32_t *block_tables,
+                             const int32_t *context_lens, const int32_t *query_start,
+                             const uint64_t *tree_masks, int mask_words, int num_seqs,
+                             int num_tokens, int max_blocks_per_seq, int num_q_heads,
+                             int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                             float scale, float k_scale, float v_scale, const float *k_scales,
+                             const float *v_scales, int max_query_len, void *workspace,
+                             size_t workspace_bytes, int32_t *err_flag, void *stream);
+
+/*
+ * paged_tree_commit -- for every sequence s and r < accepted_lens[s], the K and V rows of
+ * tree token accepted[s][r] (int32 [num_seqs][max_accept]; it stands at slot
+ * slot_mapping[query_start[s] + accepted[s][r]]) are copied, bit for bit and for all KV
+ * heads, to slot dst_slots[s][r] (int64 [num_seqs][max_accept]) or, dst_slots NULL, to
+ * slot_mapping[query_start[s] + r].  Within a sequence every row is read before any is
+ * written, so the path may overlap its destinations and come in any order; a destination may
+ * not repeat, nor be another sequence's source or destination.  A negative source or
+ * destination slot skips the row.  An index outside [0, L) sets PKV_DEV_BAD_ROW, a slot
+ * outside the pool PKV_DEV_BAD_SLOT, and the row is skipped; accepted_lens[s] outside
+ * [0, max_accept] (or above L without dst_slots) sets PKV_DEV_BAD_CONTEXT and moves nothing
+ * of s.  max_accept <= PKV_TREE_MAX_TOKENS; head_dim 64 or 128.
+ */
+int paged_tree_commit(uint16_t *k_cache, uint16_t *v_cache, const int64_t *slot_mapping,
+                      const int32_t *query_start, const int32_t *accepted,
+                      const int32_t *accepted_lens, const int64_t *dst_slots, int num_seqs,
+                      int num_tokens, int max_accept, int num_blocks, int num_kv_heads,
+                      int head_dim, int block_size, int32_t *err_flag, void *stream);
+int paged_tree_commit_fp8(uint8_t *k_cache, uint8_t *v_cache, const int64_t *slot_mapping,
+                          const int32_t *query_start, const int32_t *accepted,
+                          const int32_t *accepted_lens, const int64_t *dst_slots, int num_seqs,
+                          int num_tokens, int max_accept, int num_blocks, int num_kv_heads,
+                          int head_dim, int block_size, int32_t *err_flag, void *stream);
 
 /*
  * Chunked-prefill kernel selection, process-wide (for measurement; default AUTO = the

@@ -1,0 +1,250 @@
+// The two ends of a drafted-tree step: ancestor masks and positions of the drafted tokens
+// before attention, and the move of the accepted path's K/V rows after it.
+//
+// Masks.  Token i of a sequence's tree has parent p(i) < i (-1: the cached context).  It
+// attends to itself and its ancestors, mask(i) = bit i | mask(p(i)), and stands at position
+// base + depth, depth = |mask(i)| - 1.  One CTA per sequence, one thread per token, pointer
+// jumping: after round k a row holds its nearest 2^k ancestors and jump(i) the next one, so
+// ceil(log2(depth + 1)) rounds of  row(i) |= row(jump(i)), jump(i) = jump(jump(i))  finish
+// any tree.  The bytes are a few per token; the time is the launch and two dependent reads.
+//
+// Commit.  Each (sequence, KV head, cache, 128-byte slice of the rows) is one CTA that reads
+// every accepted row into shared memory, waits, and writes them out, so a path may overlap
+// the slots it moves to.  Latency-bound: lengths, path, slots, rows are dependent reads.
+#include "pkv_common.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kMaxWords = PKV_TREE_MAX_TOKENS / 64;
+
+__global__ void __launch_bounds__(PKV_TREE_MAX_TOKENS)
+    tree_masks_kernel(uint64_t *masks, int32_t *positions, const int32_t *parents,
+                      const int32_t *query_start, const int32_t *context_lens,
+                      const int32_t *position_base, int num_tokens, int W, int32_t *err) {
+  extern __shared__ uint64_t rows[];  // [64 W][W], then int jump[64 W]
+  int *jump = reinterpret_cast<int *>(rows + (size_t)64 * W * W);
+  pdl_trigger();
+  pdl_wait();
+  const int s = blockIdx.x, i = threadIdx.x;
+  const int q0 = query_start[s], q1 = query_start[s + 1], ctx = context_lens[s];
+  const int64_t L64 = (int64_t)q1 - q0;
+  if (q0 < 0 || q1 > num_tokens || L64 < 0 || L64 > 64 * W || L64 > ctx) {
+    if (i == 0) flag_error(err, PKV_DEV_BAD_CONTEXT);
+    return;
+  }
+  const int L = (int)L64;
+  if (L == 0) return;
+  int j = -1;
+  if (i < L) {
+    j = parents[q0 + i];
+    if (j < -1 || j >= i) {
+      flag_error(err, PKV_DEV_BAD_TREE);
+      j = -1;
+    }
+    for (int w = 0; w < W; ++w) rows[(size_t)i * W + w] = w == (i >> 6) ? 1ull << (i & 63) : 0ull;
+    jump[i] = j;
+  }
+  while (__syncthreads_or(j >= 0)) {
+    uint64_t r[kMaxWords];
+    int nj = -1;
+    if (j >= 0) {
+#pragma unroll
+      for (int w = 0; w < kMaxWords; ++w)
+        if (w <= (j >> 6)) r[w] = rows[(size_t)j * W + w];
+      nj = jump[j];
+    }
+    __syncthreads();
+    if (j >= 0) {
+#pragma unroll
+      for (int w = 0; w < kMaxWords; ++w)
+        if (w <= (j >> 6)) rows[(size_t)i * W + w] |= r[w];
+      jump[i] = nj;
+    }
+    j = nj;
+  }
+  for (int e = i; e < L * W; e += blockDim.x) masks[(size_t)q0 * W + e] = rows[e];
+  if (positions != nullptr && i < L) {
+    int depth = -1;
+    for (int w = 0; w < W; ++w) depth += __popcll(rows[(size_t)i * W + w]);
+    positions[q0 + i] = (position_base ? position_base[s] : ctx - L) + depth;
+  }
+}
+
+struct CommitArgs {
+  uint8_t *k_cache, *v_cache;
+  const int64_t *slots;     // [T] slots of the drafted tokens
+  const int64_t *dst_slots; // [S][A] or null (the sequence's own first slots)
+  const int32_t *query_start, *accepted, *accepted_lens;
+  int num_tokens, max_accept, heads, head_dim, elem;
+  int64_t num_slots;
+  int v_transposed;         // E4M3 V: [D][16] within a block
+  int32_t *err;
+};
+
+constexpr int kSlice = 128;         // bytes of a row one CTA moves
+constexpr int kCommitThreads = 128;
+
+__global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const CommitArgs a) {
+  extern __shared__ __align__(16) uint8_t stage[];  // [max_accept][kSlice]
+  pdl_trigger();
+  pdl_wait();
+  const int s = blockIdx.x, h = blockIdx.y;
+  const bool is_v = (blockIdx.z & 1) != 0;
+  const int slice = blockIdx.z >> 1;
+  const int q0 = a.query_start[s], q1 = a.query_start[s + 1], n = a.accepted_lens[s];
+  if (n == 0) return;
+  const int64_t L = (int64_t)q1 - q0;
+  if (q0 < 0 || L < 0 || q1 > a.num_tokens || n < 0 || n > a.max_accept ||
+      (a.dst_slots == nullptr && n > L)) {
+    if (threadIdx.x == 0) flag_error(a.err, PKV_DEV_BAD_CONTEXT);
+    return;
+  }
+  // Source and destination slots of accepted row r; false: the row is not moved.
+  auto slots_of = [&](int r, int64_t &src, int64_t &dst) {
+    const int idx = a.accepted[(size_t)s * a.max_accept + r];
+    if (idx < 0 || idx >= L) {
+      flag_error(a.err, PKV_DEV_BAD_ROW);
+      return false;
+    }
+    src = a.slots[q0 + idx];
+    dst = a.dst_slots ? a.dst_slots[(size_t)s * a.max_accept + r] : a.slots[q0 + r];
+    if (src >= a.num_slots || dst >= a.num_slots) {
+      flag_error(a.err, PKV_DEV_BAD_SLOT);
+      return false;
+    }
+    return src >= 0 && dst >= 0;
+  };
+  uint8_t *cache = is_v ? a.v_cache : a.k_cache;
+  const int64_t row_bytes = (int64_t)a.head_dim * a.elem;
+  if (is_v && a.v_transposed) {
+    // thread d owns head-dim row d of the block: one byte per token
+    const int d = threadIdx.x;
+    auto at = [&](int64_t slot) {
+      return cache + (((slot >> 4) * a.heads + h) * a.head_dim + d) * kBlockSize + (slot & 15);
+    };
+    int64_t src, dst;
+    if (d < a.head_dim)
+      for (int r = 0; r < n; ++r)
+        if (slots_of(r, src, dst)) stage[r * kSlice + d] = *at(src);
+    __syncthreads();
+    if (d < a.head_dim)
+      for (int r = 0; r < n; ++r)
+        if (slots_of(r, src, dst)) *at(dst) = stage[r * kSlice + d];
+    return;
+  }
+  const int lanes = row_bytes < kSlice ? (int)(row_bytes / 16) : kSlice / 16;
+  const int e = threadIdx.x % lanes, step = kCommitThreads / lanes;
+  auto at = [&](int64_t slot) {
+    return reinterpret_cast<uint4 *>(
+        cache + (((slot >> 4) * a.heads + h) * kBlockSize + (slot & 15)) * row_bytes +
+        slice * kSlice + e * 16);
+  };
+  uint4 *st = reinterpret_cast<uint4 *>(stage);
+  int64_t src, dst;
+  for (int r = threadIdx.x / lanes; r < n; r += step)
+    if (slots_of(r, src, dst)) st[r * (kSlice / 16) + e] = *at(src);
+  __syncthreads();
+  for (int r = threadIdx.x / lanes; r < n; r += step)
+    if (slots_of(r, src, dst)) *at(dst) = st[r * (kSlice / 16) + e];
+}
+
+int commit_impl(void *k_cache, void *v_cache, const int64_t *slot_mapping,
+                const int32_t *query_start, const int32_t *accepted, const int32_t *accepted_lens,
+                const int64_t *dst_slots, int num_seqs, int num_tokens, int max_accept,
+                int num_blocks, int num_kv_heads, int head_dim, int block_size, int elem,
+                int32_t *err_flag, void *stream) {
+  if (block_size != kBlockSize) return PKV_ERR_BLOCK_SIZE;
+  if (num_seqs < 0 || num_tokens < 0 || max_accept < 0 || max_accept > PKV_TREE_MAX_TOKENS ||
+      num_blocks <= 0 || num_kv_heads <= 0 || num_kv_heads > 65535 ||
+      (head_dim != 64 && head_dim != 128))
+    return PKV_ERR_SHAPE;
+  if (num_seqs == 0 || num_tokens == 0 || max_accept == 0) return PKV_OK;
+  if (!k_cache || !v_cache || !slot_mapping || !query_start || !accepted || !accepted_lens)
+    return PKV_ERR_NULL;
+  if (!aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_ALIGN;
+  CommitArgs a;
+  a.k_cache = static_cast<uint8_t *>(k_cache);
+  a.v_cache = static_cast<uint8_t *>(v_cache);
+  a.slots = slot_mapping;
+  a.dst_slots = dst_slots;
+  a.query_start = query_start;
+  a.accepted = accepted;
+  a.accepted_lens = accepted_lens;
+  a.num_tokens = num_tokens;
+  a.max_accept = max_accept;
+  a.heads = num_kv_heads;
+  a.head_dim = head_dim;
+  a.elem = elem;
+  a.num_slots = (int64_t)num_blocks * kBlockSize;
+  a.v_transposed = elem == 1;
+  a.err = err_flag;
+  static std::atomic<int> ready[kMaxDevices];
+  const int r = per_device_setup(ready, [] {
+    return cudaFuncSetAttribute(tree_commit_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                PKV_TREE_MAX_TOKENS * kSlice) == cudaSuccess
+               ? 1
+               : -1;
+  });
+  if (r <= 0) return PKV_ERR_CUDA;
+  const int slices = (head_dim * elem + kSlice - 1) / kSlice;
+  const cudaError_t e = launch_pdl(
+      tree_commit_kernel,
+      dim3((unsigned)num_seqs, (unsigned)num_kv_heads, (unsigned)(2 * slices)),
+      dim3(kCommitThreads), (size_t)max_accept * kSlice, (cudaStream_t)stream, a);
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" {
+
+int paged_tree_masks(uint64_t *masks, int32_t *positions, const int32_t *parents,
+                     const int32_t *query_start, const int32_t *context_lens,
+                     const int32_t *position_base, int num_seqs, int num_tokens, int mask_words,
+                     int32_t *err_flag, void *stream) {
+  if (num_seqs < 0 || num_tokens < 0 || mask_words <= 0 || mask_words > kMaxWords)
+    return PKV_ERR_SHAPE;
+  if (num_seqs == 0 || num_tokens == 0) return PKV_OK;
+  if (!masks || !parents || !query_start || !context_lens) return PKV_ERR_NULL;
+  static std::atomic<int> ready[kMaxDevices];
+  constexpr int kMost = 64 * kMaxWords * (kMaxWords * 8 + 4);
+  const int r = per_device_setup(ready, [] {
+    return cudaFuncSetAttribute(tree_masks_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kMost) == cudaSuccess
+               ? 1
+               : -1;
+  });
+  if (r <= 0) return PKV_ERR_CUDA;
+  const cudaError_t e =
+      launch_pdl(tree_masks_kernel, dim3((unsigned)num_seqs), dim3(64 * mask_words),
+                 (size_t)64 * mask_words * (mask_words * 8 + 4), (cudaStream_t)stream, masks,
+                 positions, parents, query_start, context_lens, position_base, num_tokens,
+                 mask_words, err_flag);
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+int paged_tree_commit(uint16_t *k_cache, uint16_t *v_cache, const int64_t *slot_mapping,
+                      const int32_t *query_start, const int32_t *accepted,
+                      const int32_t *accepted_lens, const int64_t *dst_slots, int num_seqs,
+                      int num_tokens, int max_accept, int num_blocks, int num_kv_heads,
+                      int head_dim, int block_size, int32_t *err_flag, void *stream) {
+  return commit_impl(k_cache, v_cache, slot_mapping, query_start, accepted, accepted_lens,
+                     dst_slots, num_seqs, num_tokens, max_accept, num_blocks, num_kv_heads,
+                     head_dim, block_size, 2, err_flag, stream);
+}
+
+int paged_tree_commit_fp8(uint8_t *k_cache, uint8_t *v_cache, const int64_t *slot_mapping,
+                          const int32_t *query_start, const int32_t *accepted,
+                          const int32_t *accepted_lens, const int64_t *dst_slots, int num_seqs,
+                          int num_tokens, int max_accept, int num_blocks, int num_kv_heads,
+                          int head_dim, int block_size, int32_t *err_flag, void *stream) {
+  return commit_impl(k_cache, v_cache, slot_mapping, query_start, accepted, accepted_lens,
+                     dst_slots, num_seqs, num_tokens, max_accept, num_blocks, num_kv_heads,
+                     head_dim, block_size, 1, err_flag, stream);
+}
+
+}  // extern "C"

@@ -19,13 +19,14 @@ PKV_ATTN_AUTO, PKV_ATTN_FMA, PKV_ATTN_MMA = 0, 1, 2
 PKV_PREFILL_AUTO, PKV_PREFILL_MMA, PKV_PREFILL_TC, PKV_PREFILL_TC_PAIR = 0, 1, 2, 3
 PKV_PREFILL_TC_2SM, PKV_PREFILL_TC_SEP = 4, 5
 DEV_BAD_BLOCK, DEV_BAD_SLOT, DEV_BAD_CONTEXT, DEV_TIMEOUT = 1, 2, 4, 8
-DEV_BAD_SCALE, DEV_BAD_ROW = 32, 64
+DEV_BAD_SCALE, DEV_BAD_ROW, DEV_BAD_TREE = 32, 64, 128
+TREE_MAX_TOKENS = 1024
 DEFAULT_PARTITION = 512
 
 # Every entry point the header declares: name -> (restype, argtypes).
 _P, _I, _F, _SZ, _I64 = (ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t,
                          ctypes.c_int64)
-ABI_VERSION = 4  # PKV_ABI_VERSION of include/pagedkv.h
+ABI_VERSION = 5  # PKV_ABI_VERSION of include/pagedkv.h
 SIGNATURES = {
     "paged_kv_version": (_I, []),
     "paged_kv_strerror": (ctypes.c_char_p, [_I]),
@@ -54,6 +55,21 @@ SIGNATURES = {
                                                  _I, _F, _P, _P, _I, _I, _P, _SZ, _P, _P]),
     "paged_attention_prefill": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I,
                                      _F, _I, _P, _P]),
+    "paged_tree_masks": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P]),
+    "paged_qk_norm_rope_write": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _F, _P,
+                                      _I64, _I, _P, _P, _I, _I, _F, _P, _I, _P, _P, _I, _I, _I,
+                                      _I, _I, _P, _P]),
+    "paged_qk_norm_rope_write_fp8": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _F,
+                                          _P, _I64, _I, _P, _P, _I, _I, _F, _P, _I, _P, _P, _I,
+                                          _I, _I, _I, _I, _F, _F, _P, _P, _P, _P]),
+    "paged_attention_tree_workspace_size": (_SZ, [_I, _I, _I, _I]),
+    "paged_attention_tree": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I,
+                                  _I, _F, _I, _P, _SZ, _P, _P]),
+    "paged_attention_tree_fp8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I,
+                                      _I, _I, _F, _F, _F, _P, _P, _I, _P, _SZ, _P, _P]),
+    "paged_tree_commit": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P]),
+    "paged_tree_commit_fp8": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P,
+                                   _P]),
     "pkv_pool_create": (_I, [_I, _I, _P, ctypes.POINTER(_P)]),
     "pkv_pool_destroy": (None, [_P]),
     "pkv_pool_num_free": (_I, [_P]),
@@ -459,3 +475,272 @@ def paged_decode_step_fp8(out, q, k_cache, v_cache, block_tables, context_lens, 
         _ptr(v_new) if T else None, _ptr(slot_mapping) if T else None, T,
         _ptr(block_pairs) if P else None, P, _ptr(workspace), workspace.numel(),
         _ptr(err_flag), _stream(stream)), "paged_decode_step_fp8")
+
+
+# ---- drafted trees -------------------------------------------------------------------
+def _call(name, stream, first, others, *args):
+    """Run entry point `name` on the device that holds `first` (and must hold every tensor
+    of `others`), on `stream` or that device's current stream."""
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name}: every tensor must be on {dev}, got one on {t.device}")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev).cuda_stream
+    elif hasattr(stream, "cuda_stream"):
+        if stream.device != dev:
+            raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on {dev}")
+        stream = stream.cuda_stream
+    if dev.index == torch.cuda.current_device():
+        check(getattr(lib, name)(*args, int(stream)), name)
+    else:
+        with torch.cuda.device(dev):
+            check(getattr(lib, name)(*args, int(stream)), name)
+
+
+def _i64(name, t):
+    if t.dtype != torch.int64 or not t.is_cuda or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous int64 CUDA tensor")
+
+
+def _err_word(t):
+    if t is not None and (t.dtype != torch.int32 or not t.is_cuda or t.numel() < 1):
+        raise TypeError("err_flag must be an int32 CUDA tensor")
+
+
+def _caches(k_cache, v_cache, f8):
+    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        (_u8_cuda if f8 else _bf16_cuda)(n, t)
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must be [num_blocks][num_kv_heads][16][head_dim]")
+    return k_cache.shape
+
+
+def _scale_args(k_scale, v_scale, num_kv_heads):
+    """(k_scale, v_scale, k_scales pointer, v_scales pointer, tensors) of an E4M3 call."""
+    if torch.is_tensor(k_scale) or torch.is_tensor(v_scale):
+        if not (torch.is_tensor(k_scale) and torch.is_tensor(v_scale)):
+            raise TypeError("k_scale and v_scale must both be numbers or both be tensors")
+        _scales_cuda("k_scales", k_scale, num_kv_heads)
+        _scales_cuda("v_scales", v_scale, num_kv_heads)
+        return 1.0, 1.0, k_scale.data_ptr(), v_scale.data_ptr(), (k_scale, v_scale)
+    return float(k_scale), float(v_scale), None, None, ()
+
+
+def paged_tree_masks(masks, positions, parents, query_start, context_lens, position_base=None,
+                     err_flag=None, stream=None):
+    """Ancestor bit masks (int64 [T][W], bit b of word w = tree token 64 w + b) and positions
+    (int32 [T] or None) of drafted trees from each token's parent (int32 [T], -1 = the cached
+    context).  A tree token's position is position_base[s] (default: where the tree starts in
+    the context) plus its depth."""
+    _i64("masks", masks)
+    _i32("parents", parents)
+    _i32("query_start", query_start)
+    _i32("context_lens", context_lens)
+    _err_word(err_flag)
+    T, S = parents.shape[0], context_lens.shape[0]
+    if masks.dim() != 2 or masks.shape[0] != T or query_start.shape != (S + 1,):
+        raise ValueError("masks must be [num_tokens][words] and query_start [S+1]")
+    if positions is not None:
+        _i32("positions", positions)
+        if positions.shape != (T,):
+            raise ValueError("positions must be [num_tokens]")
+    if position_base is not None:
+        _i32("position_base", position_base)
+        if position_base.shape != (S,):
+            raise ValueError("position_base must be [S]")
+    _call("paged_tree_masks", stream, masks,
+          (positions, parents, query_start, context_lens, position_base, err_flag),
+          masks.data_ptr(), _ptr(positions), parents.data_ptr(), query_start.data_ptr(),
+          context_lens.data_ptr(), _ptr(position_base), S, T, masks.shape[1], _ptr(err_flag))
+
+
+def _head_rows(name, t, T, D):
+    """Heads and token stride of a [T][H][D] bf16 tensor whose heads are adjacent."""
+    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 3:
+        raise TypeError(f"{name} must be a bf16 CUDA tensor [num_tokens][heads][head_dim]")
+    H = t.shape[1]
+    if t.shape[0] != T or t.shape[2] != D:
+        raise ValueError(f"{name} must be [num_tokens][heads][head_dim]")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (H > 1 and s1 != D):
+        raise ValueError(f"{name}: heads must be adjacent rows of head_dim elements")
+    return H, (s0 if T > 1 else H * D)
+
+
+def _qk_norm_rope_write(name, f8, q_out, q, k, v, positions, inv_freq, slot_mapping, k_cache,
+                        v_cache, scales, q_weight, k_weight, eps, pair_axes, interleaved,
+                        rope_scale, err_flag, stream):
+    NB, Hkv, bs, D = _caches(k_cache, v_cache, f8)
+    _i64("slot_mapping", slot_mapping)
+    _err_word(err_flag)
+    T = slot_mapping.shape[0]
+    Hq, qs = _head_rows("q", q, T, D)
+    Ho, os_ = _head_rows("q_out", q_out, T, D)
+    Hk, ks = _head_rows("k", k, T, D)
+    Hv, vs = _head_rows("v", v, T, D)
+    if Ho != Hq or Hk != Hkv or Hv != Hkv:
+        raise ValueError("q_out must have q's heads; k and v the cache's")
+    for n, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _bf16_cuda(n, w)
+            if w.shape != (D,):
+                raise ValueError(f"{n} must be [head_dim]")
+    half = axes = stride = 0
+    if inv_freq is not None:
+        half = inv_freq.numel()
+        if inv_freq.dtype != torch.float64 or not inv_freq.is_cuda or not inv_freq.is_contiguous():
+            raise TypeError("inv_freq must be a contiguous float64 CUDA tensor")
+        if positions is None or positions.dtype != torch.int32 or not positions.is_cuda:
+            raise TypeError("positions must be an int32 CUDA tensor")
+        if positions.dim() not in (1, 2) or positions.shape[-1] != T or (
+                T > 1 and positions.stride(-1) != 1):
+            raise ValueError("positions must be [num_tokens] or [axes][num_tokens]")
+        axes = positions.shape[0] if positions.dim() == 2 else 1
+        stride = positions.stride(0) if axes > 1 else 0
+    if pair_axes is not None:
+        if not isinstance(pair_axes, bytes):
+            pair_axes = bytes([int(x) for x in pair_axes])
+        if len(pair_axes) != half:
+            raise ValueError("pair_axes must name an axis for each of inv_freq's pairs")
+    elif axes > 1:
+        raise ValueError("positions with several axes need pair_axes")
+    tail = () if scales is None else scales[:4]
+    _call(name, stream, q, (q_out, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache,
+                            q_weight, k_weight, err_flag, *(scales[4] if scales else ())),
+          q_out.data_ptr(), os_, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+          _ptr(q_weight), _ptr(k_weight), eps, _ptr(positions) if half else None, stride,
+          max(axes, 1), pair_axes, _ptr(inv_freq), 2 * half, 1 if interleaved else 0, rope_scale,
+          slot_mapping.data_ptr(), T, k_cache.data_ptr(), v_cache.data_ptr(), NB, Hq, Hkv, D, bs,
+          *tail, _ptr(err_flag))
+
+
+def paged_qk_norm_rope_write(q_out, q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache,
+                             q_weight=None, k_weight=None, eps=1e-6, pair_axes=None,
+                             interleaved=False, rope_scale=1.0, err_flag=None, stream=None):
+    """Head-wise RMS norm (with weights [D]) and rotary positions of q into q_out and of k into
+    the cache at slot_mapping, v into the cache.  q, k, v, q_out: [T][heads][D], tokens any
+    stride apart (slices of one projection).  inv_freq: float64 [pairs] radians per position
+    (None: no rotation); positions: int32 [T] or [axes][T]; pair_axes: the axis of each pair
+    (bytes or a sequence of ints) when there are several.  q_out may be q."""
+    _qk_norm_rope_write("paged_qk_norm_rope_write", False, q_out, q, k, v, positions, inv_freq,
+                        slot_mapping, k_cache, v_cache, None, q_weight, k_weight, eps, pair_axes,
+                        interleaved, rope_scale, err_flag, stream)
+
+
+def paged_qk_norm_rope_write_fp8(q_out, q, k, v, positions, inv_freq, slot_mapping, k_cache,
+                                 v_cache, k_scale, v_scale, q_weight=None, k_weight=None,
+                                 eps=1e-6, pair_axes=None, interleaved=False, rope_scale=1.0,
+                                 err_flag=None, stream=None):
+    """paged_qk_norm_rope_write into E4M3 caches.  k_scale/v_scale: floats (one scale per
+    cache) or float32 CUDA tensors [num_kv_heads] (one scale per KV head)."""
+    scales = _scale_args(k_scale, v_scale, k_cache.shape[1])
+    _qk_norm_rope_write("paged_qk_norm_rope_write_fp8", True, q_out, q, k, v, positions, inv_freq,
+                        slot_mapping, k_cache, v_cache, scales, q_weight, k_weight, eps,
+                        pair_axes, interleaved, rope_scale, err_flag, stream)
+
+
+def paged_attention_tree_workspace_size(num_q_heads, num_kv_heads, head_dim,
+                                        max_query_len) -> int:
+    """Bytes paged_attention_tree needs on the current device."""
+    return int(lib.paged_attention_tree_workspace_size(num_q_heads, num_kv_heads, head_dim,
+                                                       max_query_len))
+
+
+def alloc_tree_workspace(num_q_heads, num_kv_heads, head_dim, max_query_len, device="cuda"):
+    """Scratch for paged_attention_tree calls of these sizes on `device` (any number of
+    sequences and any context lengths)."""
+    with torch.cuda.device(device):
+        n = paged_attention_tree_workspace_size(num_q_heads, num_kv_heads, head_dim,
+                                                max_query_len)
+    if n == 0:
+        raise ValueError("head counts, head_dim or max_query_len out of range")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _attention_tree(name, f8, out, q, k_cache, v_cache, block_tables, context_lens, query_start,
+                    tree_masks, scale, scales, max_query_len, workspace, err_flag, stream):
+    NB, Hkv, bs, D = _caches(k_cache, v_cache, f8)
+    _bf16_cuda("out", out)
+    _bf16_cuda("q", q)
+    _i32("block_tables", block_tables)
+    _i32("context_lens", context_lens)
+    _i32("query_start", query_start)
+    _i64("tree_masks", tree_masks)
+    _err_word(err_flag)
+    S = context_lens.shape[0]
+    if q.dim() != 3 or q.shape[2] != D or out.shape != q.shape:
+        raise ValueError("q and out must be [num_tokens][num_q_heads][head_dim]")
+    T, Hq, _ = q.shape
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or query_start.shape != (S + 1,):
+        raise ValueError("block_tables must be [S][max_blocks] and query_start [S+1]")
+    if tree_masks.dim() != 2 or tree_masks.shape[0] != T:
+        raise ValueError("tree_masks must be [num_tokens][words]")
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous CUDA tensor")
+    kv_scales = () if scales is None else scales[:4]
+    _call(name, stream, q, (out, k_cache, v_cache, block_tables, context_lens, query_start,
+                            tree_masks, workspace, err_flag, *(scales[4] if scales else ())),
+          out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+          block_tables.data_ptr(), context_lens.data_ptr(), query_start.data_ptr(),
+          tree_masks.data_ptr(), tree_masks.shape[1], S, T, block_tables.shape[1], Hq, Hkv, D, bs,
+          NB, scale, *kv_scales, max_query_len, workspace.data_ptr(),
+          workspace.numel() * workspace.element_size(), _ptr(err_flag))
+
+
+def paged_attention_tree(out, q, k_cache, v_cache, block_tables, context_lens, query_start,
+                         tree_masks, scale, max_query_len, workspace, err_flag=None, stream=None):
+    """Attention of drafted trees: rows query_start[s] .. query_start[s+1]-1 of q [T][Hq][D]
+    are the last tokens of sequence s; each sees the cached tokens before the tree and the tree
+    tokens its tree_masks row (int64 [T][W]) names.  workspace: alloc_tree_workspace."""
+    _attention_tree("paged_attention_tree", False, out, q, k_cache, v_cache, block_tables,
+                    context_lens, query_start, tree_masks, scale, None, max_query_len, workspace,
+                    err_flag, stream)
+
+
+def paged_attention_tree_fp8(out, q, k_cache, v_cache, block_tables, context_lens, query_start,
+                             tree_masks, scale, k_scale, v_scale, max_query_len, workspace,
+                             err_flag=None, stream=None):
+    """paged_attention_tree over E4M3 caches.  k_scale/v_scale: floats (one scale per cache)
+    or float32 CUDA tensors [num_kv_heads] (one scale per KV head)."""
+    scales = _scale_args(k_scale, v_scale, k_cache.shape[1])
+    _attention_tree("paged_attention_tree_fp8", True, out, q, k_cache, v_cache, block_tables,
+                    context_lens, query_start, tree_masks, scale, scales, max_query_len,
+                    workspace, err_flag, stream)
+
+
+def _tree_commit(name, f8, k_cache, v_cache, slot_mapping, query_start, accepted, accepted_lens,
+                 dst_slots, err_flag, stream):
+    NB, Hkv, bs, D = _caches(k_cache, v_cache, f8)
+    _i64("slot_mapping", slot_mapping)
+    _i32("query_start", query_start)
+    _i32("accepted", accepted)
+    _i32("accepted_lens", accepted_lens)
+    _err_word(err_flag)
+    S = accepted_lens.shape[0]
+    if accepted.dim() != 2 or accepted.shape[0] != S or query_start.shape != (S + 1,):
+        raise ValueError("accepted must be [S][max_accept] and query_start [S+1]")
+    if dst_slots is not None:
+        _i64("dst_slots", dst_slots)
+        if dst_slots.shape != accepted.shape:
+            raise ValueError("dst_slots must have accepted's shape")
+    _call(name, stream, k_cache, (v_cache, slot_mapping, query_start, accepted, accepted_lens,
+                                  dst_slots, err_flag),
+          k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), query_start.data_ptr(),
+          accepted.data_ptr(), accepted_lens.data_ptr(), _ptr(dst_slots), S,
+          slot_mapping.shape[0], accepted.shape[1], NB, Hkv, D, bs, _ptr(err_flag))
+
+
+def paged_tree_commit(k_cache, v_cache, slot_mapping, query_start, accepted, accepted_lens,
+                      dst_slots=None, err_flag=None, stream=None):
+    """Move the K/V rows of each sequence's accepted tree tokens (accepted int32 [S][A], the
+    first accepted_lens[s] of row s) to the tree's first slots, or to dst_slots [S][A]."""
+    _tree_commit("paged_tree_commit", False, k_cache, v_cache, slot_mapping, query_start, accepted,
+                 accepted_lens, dst_slots, err_flag, stream)
+
+
+def paged_tree_commit_fp8(k_cache, v_cache, slot_mapping, query_start, accepted, accepted_lens,
+                          dst_slots=None, err_flag=None, stream=None):
+    """paged_tree_commit over E4M3 caches."""
+    _tree_commit("paged_tree_commit_fp8", True, k_cache, v_cache, slot_mapping, query_start,
+                 accepted, accepted_lens, dst_slots, err_flag, stream)
