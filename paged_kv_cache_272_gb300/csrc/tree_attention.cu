@@ -1,4 +1,4 @@
-// Attention of a tree of drafted tokens over the paged cache.
+// Attention of a tree of drafted tokens over the paged cache, on tcgen05 tensor cores.
 //
 // Sequence s has L drafted tokens, the last L of its context_lens[s] cached tokens.  Token i
 // sees every cached token before the tree and the tree tokens its mask row names:
@@ -6,18 +6,58 @@
 // over those t; a token that sees nothing gives zeros.  A masked K or V row takes no part
 // whatever it holds.
 //
-// One warp per (drafted token, query head) walks the keys with a running maximum and sum.
+// Rows.  The (token, query head) pairs that share one KV head are the rows of a product:
+// row r is token r / G and head r % G of the group, 128 rows to a tile.  Keys come in tiles
+// of 64.  One CTA runs a list of (sequence, KV head, row tile, key range) segments:
+//  * warps 0-3 ("softmax"): thread t owns row t (TMEM lane t).  They stage Q (the first 64
+//    head-dim columns in TMEM, the others in shared memory), read each score tile, mask it,
+//    keep the running maximum and sum in fp32, write the weights to TMEM, rescale the output
+//    accumulator when the maximum grows by more than 2^8, and finish a segment.  A warp whose
+//    rows are all past the tree only keeps the barriers going.
+//  * warp 4 issues S = Q K^T, warp 7 O += P V (one lane each; issuing takes longer than the
+//    product runs, so neither waits behind the other).
+//  * warps 5 and 6 fill the K and the V ring: TMA tiled copies of the blocks the table names
+//    (bf16), or bulk copies of the E4M3 codes that the warp then widens to f16 (exact) into
+//    the ring.
+//
+// Split.  With few rows the work is reading the cache, and a batch may be one long sequence
+// or many short ones.  So the key tiles of all (sequence, KV head) pairs of a row tile are
+// laid end to end and cut into equal runs, one per resident CTA: every CTA reads the same
+// amount, whatever the lengths.  A pair cut by a run's end leaves normalised fp32 partial
+// results (at most two per CTA, so the workspace does not grow with the batch) that
+// tree_merge_kernel joins by their log-sum-exp in the order of the keys; nothing is summed
+// in an order that depends on timing.  Each CTA finds its run from context_lens by itself:
+// one launch for the attention, one for the join.  Row tiles of one pair are run in step by
+// neighbouring CTAs, so that the cache is read from DRAM once and from L2 for the others.
+//
+// Masked values.  A weight of zero times a V element that is not finite would spoil a row
+// that does not see it.  Tiles that overlap the tree (every row sees the others) are checked:
+// elements that are not finite are taken out of the product, and the rows that do see them
+// get them added at the end.
+#include <cuda.h>
 #include <math.h>
 
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <atomic>
 #include <climits>
 
-#include "pkv_common.cuh"
+#include "tcgen05.cuh"
 
 namespace pkv {
 namespace {
+
+using namespace t5;
+
+constexpr unsigned kFullMask = 0xffffffffu;
+constexpr int kTileRows = 128;
+constexpr int kTileKeys = 64;
+constexpr int kTileBlocks = kTileKeys / kBlockSize;
+constexpr int kTreeThreads = 256;
+constexpr uint32_t kTmemColumns = 256;
+constexpr int kMaxRowTiles = 64;  // row tiles of one launch
+constexpr int kMinRun = 1;        // least key tiles per CTA
 
 struct TreeArgs {
   uint16_t *out;                // [T][Hq][D] bf16
@@ -29,87 +69,919 @@ struct TreeArgs {
   const uint64_t *masks;        // [T][W]
   int num_seqs, num_tokens, max_blocks, q_heads, kv_heads, group, num_blocks, words;
   int max_query_len;
-  float scale;
-  float k_scale, v_scale;
+  float scale_log2;             // scale * log2(e) (* k_scale of an E4M3 cache)
+  float v_scale;
   const float *k_scales, *v_scales;  // [Hkv] or null
+  int runs;                     // CTAs that share the key tiles
+  int m0, row_tiles;            // this launch's row tiles m0 .. m0 + row_tiles - 1
+  int4 *join;                   // [CTAs] {s, KV head, row tile, parts}: what starts and does
+                                // not end in a CTA
+  float *part_lse;              // [CTAs][2][128] log2-sum-exp2
+  float *part_o;                // [CTAs][2][128][D] normalised
   int32_t *err;
 };
 
-__device__ __forceinline__ float e4m3(uint8_t c) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw(c, __NV_E4M3);
-  return __half2float(__half(h));
+struct SeqInfo {
+  int q0, L, ctx, tiles, row_tiles;  // tiles 0: nothing to do
+};
+
+__device__ __forceinline__ SeqInfo seq_info(const TreeArgs &a, int s, bool flag) {
+  SeqInfo i;
+  const int q1 = a.query_start[s + 1];
+  i.q0 = a.query_start[s];
+  i.ctx = a.context_lens[s];
+  const int64_t L = (int64_t)q1 - i.q0;
+  if (i.q0 < 0 || L < 0 || q1 > a.num_tokens || L > a.max_query_len || L > i.ctx ||
+      (int64_t)i.ctx > (int64_t)a.max_blocks * kBlockSize) {
+    if (flag) flag_error(a.err, PKV_DEV_BAD_CONTEXT);
+    i.L = i.tiles = i.row_tiles = 0;
+    return i;
+  }
+  i.L = (int)L;
+  i.tiles = i.L > 0 ? (int)(((int64_t)i.ctx + kTileKeys - 1) / kTileKeys) : 0;
+  i.row_tiles = (int)((L * a.group + kTileRows - 1) / kTileRows);
+  return i;
+}
+
+// A CTA's run of key tiles, filled by plan_run.
+struct Plan {
+  unsigned long long tiles[kMaxRowTiles];  // key tiles of row tile m (all KV heads)
+  unsigned long long warp_sum[kTreeThreads / 32];
+  unsigned long long off;  // first tile within sequence s (KV heads end to end)
+  long long left;          // tiles of the run
+  long long cta_tiles, extra;  // run length of this row tile's CTAs: cta_tiles, one more for
+  int ctas, cta;               // the first `extra` of its `ctas`; this CTA's number there
+  int s, m;
+};
+
+// Which key tiles this CTA runs (all threads; the result in *p after the last barrier).
+__device__ void plan_run(const TreeArgs &a, Plan *p) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid < kMaxRowTiles) p->tiles[tid] = 0;
+  if (tid == 0) p->left = 0;
+  __syncthreads();
+  unsigned long long mine = 0;  // of the last row tile of each sequence, one row tile only
+  for (int s = tid; s < a.num_seqs; s += kTreeThreads) {
+    const SeqInfo i = seq_info(a, s, blockIdx.x == 0);
+    const int last = min(i.row_tiles - a.m0, a.row_tiles);
+    if (i.tiles == 0 || last <= 0) continue;
+    if (a.row_tiles == 1)
+      mine += i.tiles;
+    else
+      atomicAdd(&p->tiles[last - 1], (unsigned long long)i.tiles);
+  }
+  if (a.row_tiles == 1) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mine += __shfl_xor_sync(kFullMask, mine, off);
+    if (lane == 0 && mine) atomicAdd(&p->tiles[0], mine);
+  }
+  __syncthreads();
+  if (tid == 0) {
+    unsigned long long sum = 0, total = 0;
+    for (int m = a.row_tiles - 1; m >= 0; --m) {
+      sum += p->tiles[m] * (unsigned)a.kv_heads;
+      p->tiles[m] = sum;
+      total += sum;
+    }
+    int at = 0;
+    for (int m = 0; m < a.row_tiles && p->tiles[m]; ++m) {
+      const unsigned long long w = p->tiles[m];
+      int n = total == w ? a.runs : (int)((double)a.runs * (double)w / (double)total);
+      const unsigned long long most = (w + kMinRun - 1) / kMinRun;
+      if ((unsigned long long)n > most) n = (int)most;
+      if (n < 1) n = 1;
+      if ((int)blockIdx.x < at + n) {
+        const int c = (int)blockIdx.x - at;
+        p->m = a.m0 + m;
+        p->ctas = n;
+        p->cta = c;
+        p->cta_tiles = (long long)(w / n);
+        p->extra = (long long)(w % n);
+        p->left = p->cta_tiles + (c < p->extra ? 1 : 0);
+        p->off = (unsigned long long)c * p->cta_tiles + min((long long)c, p->extra);
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  if (p->left == 0) return;
+  const unsigned long long u0 = p->off;
+  const int m = p->m;
+  unsigned long long base = 0;
+  for (int s0 = 0; s0 < a.num_seqs; s0 += kTreeThreads) {
+    __syncthreads();
+    const int s = s0 + tid;
+    unsigned long long n = 0;
+    if (s < a.num_seqs) {
+      const SeqInfo i = seq_info(a, s, false);
+      if (i.row_tiles > m) n = (unsigned long long)i.tiles * a.kv_heads;
+    }
+    unsigned long long incl = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const unsigned long long v = __shfl_up_sync(kFullMask, incl, off);
+      if (lane >= off) incl += v;
+    }
+    if (lane == 31) p->warp_sum[warp] = incl;
+    __syncthreads();
+    unsigned long long before = base, all = base;
+    for (int w = 0; w < kTreeThreads / 32; ++w) {
+      if (w < warp) before += p->warp_sum[w];
+      all += p->warp_sum[w];
+    }
+    const unsigned long long first = before + incl - n;
+    if (n && u0 >= first && u0 < first + n) {
+      p->s = s;
+      p->off = u0 - first;
+    }
+    base = all;
+    if (u0 < all) break;
+  }
+  __syncthreads();
+}
+
+// The segments of a run in order; every warp walks them for itself.
+struct Segment {
+  int s, g, q0, L, ctx, tiles, j0, j1;
+};
+
+struct Walk {
+  const TreeArgs &a;
+  long long left;
+  int m, s, g, tile;
+  SeqInfo i;
+  __device__ Walk(const TreeArgs &args, const Plan &p)
+      : a(args), left(p.left), m(p.m), s(p.s), g(0), tile(0) {
+    if (left > 0) {
+      i = seq_info(a, s, false);
+      g = (int)(p.off / i.tiles);
+      tile = (int)(p.off % i.tiles);
+    }
+  }
+  __device__ bool next(Segment &o) {
+    if (left <= 0) return false;
+    if (g == a.kv_heads) {
+      g = 0;
+      do {
+        if (++s >= a.num_seqs) return false;  // not reached: the run's tiles are counted
+        i = seq_info(a, s, false);
+      } while (i.tiles == 0 || i.row_tiles <= m);
+    }
+    o.s = s, o.g = g, o.q0 = i.q0, o.L = i.L, o.ctx = i.ctx, o.tiles = i.tiles;
+    o.j0 = tile;
+    o.j1 = (int)min((long long)i.tiles, tile + left);
+    left -= o.j1 - o.j0;
+    tile = 0;
+    ++g;
+    return true;
+  }
+};
+
+// Shared memory of one CTA (two per SM).  D: head dim; NS: ring slots; F8: E4M3 cache, with
+// RS slots of staged codes.
+template <int D, bool F8>
+struct TreeLayout {
+  static constexpr int NS = F8 && D == 128 ? 2 : 3;
+  static constexpr int RS = F8 ? 2 : 0;
+  static constexpr int kHalves = D / 64;
+  static constexpr int kHalf = kTileKeys * 128;       // 64 keys x 64 columns of 2 bytes
+  static constexpr int kSlot = kHalves * kHalf;
+  static constexpr int kRaw = kTileKeys * D;          // a tile of codes
+  static constexpr int kQ = 0;                        // Q's columns 64..127
+  static constexpr int kK = (kHalves - 1) * kTileRows * 128;
+  static constexpr int kV = kK + NS * kSlot;
+  static constexpr int kRawK = kV + NS * kSlot;
+  static constexpr int kRawV = kRawK + RS * kRaw;
+  static constexpr int kBars = kRawV + RS * kRaw;
+  static constexpr int kNumBars = 4 * NS + 7 + 2 * RS;
+  static constexpr int kMisc = kBars + kNumBars * 8;  // TMEM address, abort flag, V marks
+  static constexpr int kPlan = kMisc + 96;
+  static constexpr int kSmem = kPlan + (int)sizeof(Plan);
+  // at least 78 KB, so that no more than two CTAs share an SM (256 TMEM columns each)
+  static constexpr int kSmemLaunch = kSmem > 78 * 1024 ? kSmem : 78 * 1024;
+  static_assert(2 * (kSmemLaunch + 1024) <= 228 * 1024, "two CTAs per SM");
+};
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
+  return pack_f16(bf16_lo(w), bf16_hi(w));
+}
+// Two E4M3 codes (low 16 bits) -> two f16, exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t c) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xffffu), __NV_E4M3);
+  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+__device__ __forceinline__ float e4m3_to_f32(uint8_t c) {
+  return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
+}
+
+// The bits of a row's mask for keys t0 .. t0 + 63 (bit c: key t0 + c is visible): cached
+// tokens before the tree, and the tree tokens the row names.
+__device__ __forceinline__ uint64_t visible_bits(const uint64_t *mask, int t0, int first, int L) {
+  const int o = t0 - first;  // tree index of key t0
+  if (o <= -kTileKeys) return ~0ull;
+  const int words = (L + 63) >> 6;
+  uint64_t b;
+  if (o < 0) {
+    b = ((1ull << -o) - 1) | (mask[0] << -o);
+  } else {
+    const int w = o >> 6, sh = o & 63;
+    b = w < words ? mask[w] >> sh : 0ull;
+    if (sh && w + 1 < words) b |= mask[w + 1] << (64 - sh);
+  }
+  const int end = L - o;  // keys past the tree's end
+  return end >= 64 ? b : b & ((1ull << end) - 1);
 }
 
 template <int D, bool F8>
-__global__ void __launch_bounds__(256) tree_simple_kernel(const TreeArgs a) {
+__global__ void __launch_bounds__(kTreeThreads, 2)
+    tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap tk,
+                          const __grid_constant__ CUtensorMap tv) {
+  using Lay = TreeLayout<D, F8>;
+  constexpr int H = Lay::kHalves, NS = Lay::NS, RS = Lay::RS;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uint32_t base = smem_u32(smem);
+  if (base & 1023u) {  // the swizzled tiles need a 1024-byte aligned window
+    if (threadIdx.x == 0) flag_error(a.err, PKV_DEV_LAYOUT);
+    return;
+  }
+  const uint32_t sQ = base + Lay::kQ, sK = base + Lay::kK, sV = base + Lay::kV;
+  const uint32_t k_full = base + Lay::kBars, k_empty = k_full + 8 * NS;
+  const uint32_t v_full = k_empty + 8 * NS, v_empty = v_full + 8 * NS;
+  const uint32_t s_full = v_empty + 8 * NS, s_free = s_full + 8, p_full = s_free + 8;
+  const uint32_t o_done = p_full + 8, fin_s = o_done + 8, fin_o = fin_s + 8;
+  const uint32_t q_full = fin_o + 8, rk_full = q_full + 8, rv_full = rk_full + 8 * RS;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Lay::kMisc);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  // Marks of V tiles that held a value not finite.  E4M3: [ring slot], set by the V warp for
+  // the slot's tile.  bf16: [tile of the tree], the number of the segment that found one.
+  volatile int *v_bad = abort_flag + 1;
+  constexpr int kMarks = F8 ? NS : PKV_TREE_MAX_TOKENS / kTileKeys + 1;
+  static_assert(8 + 4 * kMarks <= 96, "marks");
+  Plan *plan = reinterpret_cast<Plan *>(smem + Lay::kPlan);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(k_full + 8 * i, F8 ? 1 : kTileBlocks);
+      mbar_init(k_empty + 8 * i, 1);
+      mbar_init(v_full + 8 * i, F8 ? 1 : kTileBlocks);
+      mbar_init(v_empty + 8 * i, 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(s_free, 4);
+    mbar_init(p_full, 4);
+    mbar_init(o_done, 1);
+    mbar_init(fin_s, 1);
+    mbar_init(fin_o, 1);
+    mbar_init(q_full, 4);
+    for (int i = 0; i < RS; ++i) {
+      mbar_init(rk_full + 8 * i, kTileBlocks);
+      mbar_init(rv_full + 8 * i, kTileBlocks);
+    }
+    *abort_flag = 0;
+    for (int i = 0; i < kMarks; ++i) v_bad[i] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_trigger();
+  pdl_wait();
+  plan_run(a, plan);
+  if (plan->left == 0) {
+    if (threadIdx.x == 0) a.join[blockIdx.x] = make_int4(0, 0, 0, 0);
+    return;
+  }
+  if (warp == 4) alloc(smem_u32(tmem_slot), kTmemColumns);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tS = tmem, tP = tmem + 64, tQ = tmem + 96, tO = tmem + 128;
+  const int G = a.group, r0 = plan->m * kTileRows;
+  Walk walk(a, *plan);
+  Segment seg;
+
+  if (warp < 4) {
+    // ---------------- softmax warps: thread t owns row t ----------------
+    const int t = threadIdx.x;
+    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    const int r = r0 + t;
+    int jt = 0;   // tiles done (the barriers' phases)
+    int nseg = 0; // segments begun
+    bool ok = true;
+    if (t == 0) a.join[blockIdx.x] = make_int4(0, 0, 0, 0);
+    while (ok && walk.next(seg)) {
+      ++nseg;
+      const int rows = seg.L * G;
+      const bool valid = r < rows, live = r0 + warp * 32 < rows;
+      const int i = (valid ? r : rows - 1) / G, first = seg.ctx - seg.L;
+      const size_t row = ((size_t)(seg.q0 + i) * a.q_heads + seg.g * G + r % G) * D;
+      const uint64_t *mask = a.masks + (size_t)(seg.q0 + i) * a.words;
+      float sl = a.scale_log2, vs = a.v_scale;
+      if (F8 && a.k_scales != nullptr) {
+        const float ks = a.k_scales[seg.g];
+        vs = a.v_scales[seg.g];
+        if (t == 0 && !(ks > 0.f && vs > 0.f)) flag_error(a.err, PKV_DEV_BAD_SCALE);
+        sl *= ks;
+      }
+      {
+        // Q: columns 0..63 to TMEM (two 16-bit elements per column), 64..127 to shared memory
+        const uint4 *qrow = reinterpret_cast<const uint4 *>(a.q + row);
+        uint32_t qt[32];
+#pragma unroll
+        for (int c = 0; c < 8 * H; ++c) {
+          uint4 v = valid ? qrow[c] : make_uint4(0u, 0u, 0u, 0u);
+          if (F8)
+            v = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z),
+                           bf16x2_to_f16x2(v.w));
+          if (c < 8)
+            qt[4 * c] = v.x, qt[4 * c + 1] = v.y, qt[4 * c + 2] = v.z, qt[4 * c + 3] = v.w;
+          else
+            st_shared_v4(sQ + t * 128 + (((c & 7) ^ (t & 7)) << 4), v);
+        }
+        tmem_st32(tQ + lane_base, qt);
+        wait_st();
+      }
+      fence_proxy_async();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+
+      float m = -INFINITY, l = 0.f;
+      uint32_t bad = 0;  // tree tiles whose V held a value not finite
+      const int tree_tile = first / kTileKeys;
+      for (int j = seg.j0; j < seg.j1; ++j, ++jt) {
+        const int t0 = j * kTileKeys;
+        const bool in_tree = t0 + kTileKeys > first;
+        const uint64_t bits = in_tree && valid ? visible_bits(mask, t0, first, seg.L) : ~0ull;
+        if (!mbar_wait(s_full, (uint32_t)jt & 1u, abort_flag, a.err)) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        bool p_free = j == seg.j0;  // P's columns: free once the P V before has completed
+        uint32_t pk[32];
+        if (live) {
+          uint32_t x[64];
+          {
+            uint32_t (&x0)[32] = *reinterpret_cast<uint32_t (*)[32]>(&x[0]);
+            uint32_t (&x1)[32] = *reinterpret_cast<uint32_t (*)[32]>(&x[32]);
+            tmem_ld32(tS + lane_base, x0);
+            tmem_ld32(tS + 32 + lane_base, x1);
+            wait_ld();
+          }
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free);  // the next score product may overwrite S
+          if (in_tree) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (!((bits >> c) & 1)) x[c] = __float_as_uint(-INFINITY);
+          }
+          float mxv[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) mxv[c] = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 64; c += 2)
+            mxv[(c >> 1) & 7] =
+                max3(mxv[(c >> 1) & 7], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+          const float mx = sl * max3(max3(mxv[0], mxv[1], mxv[2]), max3(mxv[3], mxv[4], mxv[5]),
+                                     fmaxf(mxv[6], mxv[7]));
+          if (j == seg.j0) {
+            m = mx;
+          } else {
+            // The reference may lag the maximum by 2^8: weights stay below 2^8 and share one
+            // reference with the sum and the output, so only a larger jump rescales those.
+            const bool need = mx > m + 8.f;
+            if (__any_sync(kFullMask, need)) {
+              if (!mbar_wait(o_done, (uint32_t)(jt - 1) & 1u, abort_flag, a.err)) {
+                ok = false;
+                break;
+              }
+              p_free = true;
+              fence_after();
+              const float mn = need ? mx : m;
+              const float corr = need ? ex2(m - mn) : 1.f;
+              m = mn;
+              l *= corr;
+#pragma unroll 1
+              for (int cc = 0; cc < D / 32; ++cc) {
+                uint32_t o[32];
+                tmem_ld32(tO + 32 * cc + lane_base, o);
+                wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+                tmem_st32(tO + 32 * cc + lane_base, o);
+              }
+              wait_st();
+            }
+          }
+          // a row that has seen nothing yet: every weight 2^-inf = 0
+          const float ref = m == -INFINITY ? 0.f : m;
+          uint64_t ps2[4];
+          const uint64_t sl2 = f32x2(sl, sl), nm2 = f32x2(-ref, -ref);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            float e0, e1;
+            f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])),
+                                  sl2, nm2),
+                        e0, e1);
+            const float p0 = ex2(e0), p1 = ex2(e1);
+            const uint64_t pp = f32x2(p0, p1);
+            ps2[c & 3] = c < 4 ? pp : add_f32x2(ps2[c & 3], pp);
+            // the product takes 16-bit weights; the sum keeps them in fp32
+            pk[c] = F8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+          }
+          float s0, s1;
+          f32x2_split(add_f32x2(add_f32x2(ps2[0], ps2[1]), add_f32x2(ps2[2], ps2[3])), s0, s1);
+          l += s0 + s1;
+        } else {
+          if (lane == 0) mbar_arrive(s_free);
+        }
+        if (in_tree) {
+          // keys past the context weigh nothing: their V (whatever it is) becomes zero, and
+          // so do values of tree tokens that are not finite (E4M3: done by the V warp)
+          const int slot = jt % NS;
+          if (!mbar_wait(v_full + 8 * slot, (uint32_t)(jt / NS) & 1u, abort_flag, a.err)) {
+            ok = false;
+            break;
+          }
+          if (!F8) {
+            const uint32_t vst = sV + slot * Lay::kSlot;
+            for (int e = t; e < kTileKeys * 8 * H; e += 128) {
+              const int key = e / (8 * H), rem = e % (8 * H);
+              const uint32_t at = vst + (rem >> 3) * Lay::kHalf + key * 128 + (rem & 7) * 16;
+              if (t0 + key >= seg.ctx) {
+                st_shared_v4(at, make_uint4(0u, 0u, 0u, 0u));
+              } else if (t0 + key >= first) {
+                uint4 v = ld_shared_v4(at);
+                uint32_t *w = &v.x;
+                bool hit = false;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  if ((w[q] & 0x7f80u) == 0x7f80u) w[q] &= 0xffff0000u, hit = true;
+                  if ((w[q] & 0x7f800000u) == 0x7f800000u) w[q] &= 0x0000ffffu, hit = true;
+                }
+                if (hit) {
+                  st_shared_v4(at, v);
+                  v_bad[j - tree_tile] = nseg;
+                }
+              }
+            }
+            fence_proxy_async();
+          } else if (v_bad[slot]) {
+            bad |= 1u << (j - tree_tile);
+          }
+        }
+        if (!p_free) {
+          if (!mbar_wait(o_done, (uint32_t)(jt - 1) & 1u, abort_flag, a.err)) {
+            ok = false;
+            break;
+          }
+          fence_after();
+        }
+        if (live) {
+          tmem_st32(tP + lane_base, pk);
+          wait_st();
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
+      }
+      if (!ok || !mbar_wait(o_done, (uint32_t)(jt - 1) & 1u, abort_flag, a.err)) {
+        ok = false;
+        break;
+      }
+      fence_after();
+      if (!live) continue;
+      if (!F8)
+        // every warp's marks precede its last arrival on p_full, and so this product's end;
+        // the next segment's follow this warp's arrival on q_full
+        for (int j = max(seg.j0, tree_tile); j < seg.j1; ++j)
+          if (v_bad[j - tree_tile] == nseg) bad |= 1u << (j - tree_tile);
+      const bool whole = seg.j0 == 0 && seg.j1 == seg.tiles;
+      const float inv = l == 0.f ? 0.f : vs / l;
+      const size_t part = ((size_t)blockIdx.x * 2 + (seg.j0 > 0 ? 0 : 1)) * kTileRows + t;
+      if (!whole && valid) a.part_lse[part] = l == 0.f ? -INFINITY : m + log2f(l);
+#pragma unroll 1
+      for (int cc = 0; cc < D / 32; ++cc) {
+        uint32_t o[32];
+        tmem_ld32(tO + 32 * cc + lane_base, o);
+        wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+        for (uint32_t todo = valid ? bad : 0u; todo; todo &= todo - 1) {
+          // the values taken out of this tile's product, for the rows that see them
+          const int t0 = (tree_tile + __ffs(todo) - 1) * kTileKeys;
+          uint64_t see = visible_bits(mask, t0, first, seg.L);
+          if (t0 < first) see &= ~((1ull << (first - t0)) - 1);
+          for (; see; see &= see - 1) {
+            const int key = t0 + __ffsll((long long)see) - 1;
+            const int blk = a.block_tables[(size_t)seg.s * a.max_blocks + key / kBlockSize];
+            if ((unsigned)blk >= (unsigned)a.num_blocks) continue;
+            const size_t tile = ((size_t)blk * a.kv_heads + seg.g) * (kBlockSize * D);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const int d = 32 * cc + e, at = key % kBlockSize;
+              const float v =
+                  F8 ? e4m3_to_f32(static_cast<const uint8_t *>(a.v_cache)[tile + d * kBlockSize + at])
+                     : bf16_to_f32(static_cast<const uint16_t *>(a.v_cache)[tile + at * D + d]);
+              if (!(fabsf(v) < INFINITY)) o[e] = __float_as_uint(__uint_as_float(o[e]) + v);
+            }
+          }
+        }
+        if (!valid) continue;
+        if (whole) {
+          uint4 *dst = reinterpret_cast<uint4 *>(a.out + row + 32 * cc);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            dst[e] = make_uint4(
+                pack_bf16(__uint_as_float(o[8 * e]), __uint_as_float(o[8 * e + 1])),
+                pack_bf16(__uint_as_float(o[8 * e + 2]), __uint_as_float(o[8 * e + 3])),
+                pack_bf16(__uint_as_float(o[8 * e + 4]), __uint_as_float(o[8 * e + 5])),
+                pack_bf16(__uint_as_float(o[8 * e + 6]), __uint_as_float(o[8 * e + 7])));
+        } else {
+          uint4 *dst = reinterpret_cast<uint4 *>(a.part_o + part * D + 32 * cc);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+      }
+      if (t == 0 && seg.j0 == 0 && !whole) {
+        // the CTAs that run the rest of this pair's key tiles
+        int parts = 1;
+        for (long long rest = seg.tiles - seg.j1; rest > 0; ++parts)
+          rest -= plan->cta_tiles + (plan->cta + parts < plan->extra ? 1 : 0);
+        a.join[blockIdx.x] = make_int4(seg.s, seg.g, plan->m, parts);
+      }
+    }
+    fence_before();
+  } else if (warp == 4) {
+    // ---------------- S warp: lane 0 issues S = Q K^T ----------------
+    constexpr uint32_t id = idesc(kTileRows, kTileKeys, F8, false);
+    int jt = 0, ok = 1;
+    for (int nseg = 0; ok && walk.next(seg); ++nseg) {
+      if (lane == 0) ok = mbar_spin_wait(q_full, (uint32_t)nseg & 1u, abort_flag, a.err);
+      ok = __shfl_sync(kFullMask, ok, 0);  // Q is staged
+      if (!ok) break;
+      fence_after();
+      for (int j = seg.j0; j < seg.j1; ++j, ++jt) {
+        const int sb = jt % NS;
+        if (lane == 0)
+          ok = mbar_spin_wait(k_full + 8 * sb, (uint32_t)(jt / NS) & 1u, abort_flag, a.err) &&
+               (jt < 1 || mbar_spin_wait(s_free, (uint32_t)(jt - 1) & 1u, abort_flag, a.err));
+        ok = __shfl_sync(kFullMask, ok, 0);
+        if (!ok) break;
+        fence_after();
+        const uint32_t kst = sK + sb * Lay::kSlot;
+        if (lane == 0) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t b = desc_sw128(kst + (kk >> 2) * Lay::kHalf + (kk & 3) * 32, 16, 1024);
+            if (kk < 4)
+              mma_ts(tS, tQ + 8 * kk, b, id, kk > 0 ? 1u : 0u);
+            else
+              mma_ss(tS, desc_sw128(sQ + (kk & 3) * 32, 16, 1024), b, id, 1u);
+          }
+          commit(s_full);
+          commit(k_empty + 8 * sb);
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) commit(fin_s);
+    __syncwarp();
+    mbar_drain(fin_s, 0);
+    fence_before();
+  } else if (warp == 7) {
+    // ---------------- P V warp: lane 0 issues O += P V ----------------
+    fence_after();
+    // bf16: V [keys][D] (MN-major); E4M3: V widened to [D][keys] (K-major)
+    constexpr uint32_t id = idesc(kTileRows, D, F8, !F8);
+    int jt = 0, ok = 1;
+    while (ok && walk.next(seg)) {
+      for (int j = seg.j0; j < seg.j1; ++j, ++jt) {
+        const int sb = jt % NS;
+        if (lane == 0)
+          ok = mbar_spin_wait(p_full, (uint32_t)jt & 1u, abort_flag, a.err) &&
+               mbar_spin_wait(v_full + 8 * sb, (uint32_t)(jt / NS) & 1u, abort_flag, a.err);
+        ok = __shfl_sync(kFullMask, ok, 0);
+        if (!ok) break;
+        fence_after();
+        const uint32_t vst = sV + sb * Lay::kSlot;
+        if (lane == 0) {
+#pragma unroll
+          for (int k = 0; k < kTileKeys / 16; ++k)
+            mma_ts(tO, tP + 8 * k,
+                   F8 ? desc_sw128(vst + 32 * k, 16, 1024)
+                      : desc_sw128(vst + 2048 * k, Lay::kHalf, 1024),
+                   id, (j > seg.j0 || k > 0) ? 1u : 0u);
+          commit(o_done);
+          commit(v_empty + 8 * sb);
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) commit(fin_o);
+    __syncwarp();
+    mbar_drain(fin_o, 0);
+    fence_before();
+  } else {
+    // ---------------- producer warps: warp 5 K, warp 6 V ----------------
+    const bool is_v = warp == 6;
+    const uint32_t full = is_v ? v_full : k_full, empty = is_v ? v_empty : k_empty;
+    const uint32_t ring = is_v ? sV : sK;
+    // one row tile: the cache is read once, its L2 lines go first; several: the row tiles of
+    // a pair share them
+    uint64_t pol;
+    if (a.row_tiles == 1)
+      asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
+    else
+      asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+    // The block of key tile j that this lane loads, or -1 (past the context, or not a block).
+    auto block_of = [&](const Segment &g, int j) {
+      const int tok = j * kTileKeys + lane * kBlockSize;
+      if (lane >= kTileBlocks || tok >= g.ctx) return -1;
+      const int blk = a.block_tables[(size_t)g.s * a.max_blocks + tok / kBlockSize];
+      if ((unsigned)blk < (unsigned)a.num_blocks) return blk;
+      flag_error(a.err, PKV_DEV_BAD_BLOCK);
+      return -1;
+    };
+    if constexpr (!F8) {
+      const CUtensorMap *map = is_v ? &tv : &tk;
+      int issued = 0;
+      if (lane < kTileBlocks) {
+        bool more = walk.next(seg);
+        int j = seg.j0;
+        int blk = more ? block_of(seg, j) : -1;
+        while (more) {
+          const int slot = issued % NS, g = seg.g, cur = blk;
+          if (++j >= seg.j1) {
+            more = walk.next(seg);
+            j = seg.j0;
+          }
+          if (more) blk = block_of(seg, j);  // one tile ahead
+          if (issued >= NS && !mbar_wait(empty + 8 * slot, (uint32_t)((issued - NS) / NS) & 1u,
+                                         abort_flag, a.err))
+            break;
+          const uint32_t bar = full + 8 * slot;
+          mbar_arrive_expect_tx(bar, cur >= 0 ? 2048u * H : 0u);
+          if (cur >= 0) {
+            const int row = (cur * a.kv_heads + g) * kBlockSize;
+            const uint32_t dst = ring + slot * Lay::kSlot + lane * 2048;
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+              tma_load_2d_hint(dst + h * Lay::kHalf, map, 64 * h, row, bar, pol);
+          }
+          ++issued;
+        }
+      }
+      __syncwarp();
+      if (lane == 0 && *abort_flag)
+        for (int j = max(0, issued - NS); j < issued; ++j)
+          mbar_drain(full + 8 * (j % NS), (uint32_t)(j / NS) & 1u);
+    } else {
+      const uint8_t *cache = static_cast<const uint8_t *>(is_v ? a.v_cache : a.k_cache);
+      const uint32_t raw = base + (is_v ? Lay::kRawV : Lay::kRawK);
+      const uint32_t raw_full = is_v ? rv_full : rk_full;
+      Walk ahead(walk);
+      Segment as;
+      bool more = ahead.next(as);
+      int aj = as.j0, issued = 0, next_blk = more ? block_of(as, aj) : -1;
+      auto issue = [&]() {  // the next tile's codes into the raw ring
+        if (!more) return;
+        const int blk = next_blk, g = as.g;
+        if (++aj >= as.j1) {
+          more = ahead.next(as);
+          aj = as.j0;
+        }
+        if (more) next_blk = block_of(as, aj);  // one tile ahead
+        if (lane < kTileBlocks) {
+          const uint32_t bar = raw_full + 8 * (issued % RS);
+          mbar_arrive_expect_tx(bar, blk >= 0 ? (uint32_t)(kBlockSize * D) : 0u);
+          if (blk >= 0)
+            bulk_load_hint(raw + (issued % RS) * Lay::kRaw + lane * (kBlockSize * D),
+                           cache + ((size_t)blk * a.kv_heads + g) * (kBlockSize * D),
+                           kBlockSize * D, bar, pol);
+        }
+        ++issued;
+      };
+      for (int i = 0; i < RS; ++i) issue();
+      int jt = 0;
+      bool ok = true;
+      while (ok && walk.next(seg)) {
+        const int first = seg.ctx - seg.L;
+        for (int j = seg.j0; j < seg.j1; ++j, ++jt) {
+          const int slot = jt % NS, rs = jt % RS, t0 = j * kTileKeys;
+          ok = mbar_wait(raw_full + 8 * rs, (uint32_t)(jt / RS) & 1u, abort_flag, a.err) &&
+               (jt < NS || mbar_wait(empty + 8 * slot, (uint32_t)((jt - NS) / NS) & 1u, abort_flag,
+                                     a.err));
+          ok = __all_sync(kFullMask, ok);
+          if (!ok) break;
+          const uint32_t src = raw + rs * Lay::kRaw, dst = ring + slot * Lay::kSlot;
+          if (!is_v) {
+            // 16 codes a lane and step -> two 16-byte chunks of the key's swizzled row.  A
+            // quarter warp takes two rows and one 64-column half of each, so that neither the
+            // loads nor the stores meet in a bank.
+#pragma unroll 4
+            for (int it = 0; it < kTileKeys * D / 512; ++it) {
+              const int e = it * 32 + lane;
+              int key, c16;  // key row, 16-code column group
+              if (H == 2) {
+                const int pair = e >> 4, q = e & 15;  // two rows, both halves
+                key = pair * 2 + ((q >> 2) & 1);
+                c16 = (((q >> 3) ^ (q >> 2)) & 1) * 4 + (q & 3);
+              } else {
+                key = e >> 2;
+                c16 = e & 3;
+              }
+              const uint4 v = ld_shared_v4(src + key * D + c16 * 16);
+              const uint32_t row = dst + (c16 >> 2) * Lay::kHalf + key * 128;
+              const int c = (c16 & 3) * 2;
+              st_shared_v4(row + (((c) ^ (key & 7)) << 4),
+                           make_uint4(e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16),
+                                      e4m3x2_to_f16x2(v.y), e4m3x2_to_f16x2(v.y >> 16)));
+              st_shared_v4(row + (((c + 1) ^ (key & 7)) << 4),
+                           make_uint4(e4m3x2_to_f16x2(v.z), e4m3x2_to_f16x2(v.z >> 16),
+                                      e4m3x2_to_f16x2(v.w), e4m3x2_to_f16x2(v.w >> 16)));
+            }
+          } else {
+            const bool in_tree = t0 + kTileKeys > first;
+            bool hit = false;
+#pragma unroll 4
+            for (int it = 0; it < kTileKeys * D / 512; ++it) {
+              const int e = it * 32 + lane, blk = e / D, d = e % D;  // head-dim row of a block
+              uint4 v = ld_shared_v4(src + e * 16);
+              if (in_tree) {
+                uint32_t *w = &v.x;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const int key = t0 + blk * kBlockSize + q * 4;
+#pragma unroll
+                  for (int b = 0; b < 4; ++b) {
+                    const uint32_t code = (w[q] >> (8 * b)) & 0x7fu;
+                    if (key + b >= seg.ctx) {
+                      w[q] &= ~(0xffu << (8 * b));
+                    } else if (code == 0x7fu && key + b >= first) {
+                      w[q] &= ~(0xffu << (8 * b));
+                      hit = true;
+                    }
+                  }
+                }
+              }
+              const uint32_t row = dst + d * 128;
+              const int c = blk * 2;
+              st_shared_v4(row + (((c) ^ (d & 7)) << 4),
+                           make_uint4(e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16),
+                                      e4m3x2_to_f16x2(v.y), e4m3x2_to_f16x2(v.y >> 16)));
+              st_shared_v4(row + (((c + 1) ^ (d & 7)) << 4),
+                           make_uint4(e4m3x2_to_f16x2(v.z), e4m3x2_to_f16x2(v.z >> 16),
+                                      e4m3x2_to_f16x2(v.w), e4m3x2_to_f16x2(v.w >> 16)));
+            }
+            const bool any = __any_sync(kFullMask, hit);
+            if (lane == 0) v_bad[slot] = any;  // read by the softmax warps after v_full
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full + 8 * slot);
+          issue();
+        }
+      }
+      __syncwarp();
+      if (lane == 0 && *abort_flag)
+        for (int j = max(0, issued - RS); j < issued; ++j)
+          mbar_drain(raw_full + 8 * (j % RS), (uint32_t)(j / RS) & 1u);
+    }
+  }
+
+  __syncthreads();
+  if (warp == 4) {
+    fence_after();
+    dealloc(tmem, kTmemColumns);
+  }
+}
+
+// Joins the parts of a (sequence, KV head, row tile) whose key tiles several CTAs ran: part 0
+// is the last segment of CTA b, part k > 0 the first segment of CTA b + k.
+//   M = max lse_k,  out = sum_k 2^(lse_k - M) o_k / sum_k 2^(lse_k - M)
+// A warp per row; the parts' results were just written and come from L2.
+constexpr int kMergeWarps = 8;
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
   constexpr int PER = D / 32;
   pdl_trigger();
   pdl_wait();
-  const int s = blockIdx.z, lane = threadIdx.x & 31;
-  const int w = blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int q0 = a.query_start[s], q1 = a.query_start[s + 1], ctx = a.context_lens[s];
-  const int64_t L = (int64_t)q1 - q0;
-  if (q0 < 0 || L < 0 || q1 > a.num_tokens || L > a.max_query_len || L > ctx ||
-      (int64_t)ctx > (int64_t)a.max_blocks * kBlockSize) {
-    if (threadIdx.x == 0) flag_error(a.err, PKV_DEV_BAD_CONTEXT);
-    return;
-  }
-  const int i = w / a.q_heads, h = w - i * a.q_heads, g = h / a.group;
-  if (i >= L) return;
-  float ks = a.k_scale, vs = a.v_scale;
-  if (F8 && a.k_scales) {
-    ks = a.k_scales[g], vs = a.v_scales[g];
-    if (!(ks > 0.f) || !(vs > 0.f)) flag_error(a.err, PKV_DEV_BAD_SCALE);
-  }
-  const size_t row = ((size_t)(q0 + i) * a.q_heads + h) * D;
-  float q[PER], acc[PER];
-  for (int e = 0; e < PER; ++e) {
-    q[e] = bf16_to_f32(a.q[row + lane + 32 * e]);
-    acc[e] = 0.f;
-  }
-  const uint64_t *mask = a.masks + (size_t)(q0 + i) * a.words;
-  const int32_t *bt = a.block_tables + (size_t)s * a.max_blocks;
-  const int first = ctx - (int)L;
-  float m = -INFINITY, l = 0.f;
-  bool any = false;
-  for (int t = 0; t < ctx; ++t) {
-    const int j = t - first;
-    if (j >= 0 && !((mask[j >> 6] >> (j & 63)) & 1)) continue;
-    const int blk = bt[t >> 4];
-    if ((unsigned)blk >= (unsigned)a.num_blocks) {
-      if (lane == 0) flag_error(a.err, PKV_DEV_BAD_BLOCK);
-      continue;
-    }
-    const size_t base = ((size_t)blk * a.kv_heads + g) * (kBlockSize * D);
-    float k[PER], v[PER], x = 0.f;
-    for (int e = 0; e < PER; ++e) {
-      const int d = lane + 32 * e;
-      if (F8) {
-        k[e] = e4m3(static_cast<const uint8_t *>(a.k_cache)[base + (t & 15) * D + d]) * ks;
-        v[e] = e4m3(static_cast<const uint8_t *>(a.v_cache)[base + d * kBlockSize + (t & 15)]) * vs;
-      } else {
-        k[e] = bf16_to_f32(static_cast<const uint16_t *>(a.k_cache)[base + (t & 15) * D + d]);
-        v[e] = bf16_to_f32(static_cast<const uint16_t *>(a.v_cache)[base + (t & 15) * D + d]);
+  const int b = blockIdx.x, lane = threadIdx.x & 31;
+  const int4 it = a.join[b];
+  if (it.w == 0) return;
+  const int t = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  const SeqInfo i = seq_info(a, it.x, false);
+  const int r = it.z * kTileRows + t, G = a.group;
+  if (r >= i.L * G) return;
+  auto part = [&](int k) {
+    return ((size_t)(b + k) * 2 + (k == 0 ? 1 : 0)) * kTileRows + t;
+  };
+  float M = -INFINITY, L = 0.f, acc[PER];
+#pragma unroll
+  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+  for (int k0 = 0; k0 < it.w; k0 += 32) {
+    const int n = min(32, it.w - k0);
+    const float x = lane < n ? __ldcg(a.part_lse + part(k0 + lane)) : -INFINITY;
+    float mb = x;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mb = fmaxf(mb, __shfl_xor_sync(kFullMask, mb, off));
+    const float mn = fmaxf(M, mb), ref = mn == -INFINITY ? 0.f : mn;
+    const float sc = M == -INFINITY ? 0.f : exp2f(M - ref);
+    M = mn;
+    const float w = lane < n ? exp2f(x - ref) : 0.f;
+    float ws = w;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) ws += __shfl_xor_sync(kFullMask, ws, off);
+    L = fmaf(L, sc, ws);
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] *= sc;
+    for (int k = 0; k < n; k += 8) {
+      float v[8][PER];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (k + u >= n) continue;
+        const float *src = a.part_o + part(k0 + k + u) * D + lane * PER;
+        if constexpr (PER == 4) {
+          const float4 f = __ldcg(reinterpret_cast<const float4 *>(src));
+          v[u][0] = f.x, v[u][1] = f.y, v[u][2] = f.z, v[u][3] = f.w;
+        } else {
+          const float2 f = __ldcg(reinterpret_cast<const float2 *>(src));
+          v[u][0] = f.x, v[u][1] = f.y;
+        }
       }
-      x = fmaf(q[e], k[e], x);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (k + u >= n) continue;
+        const float c = __shfl_sync(kFullMask, w, k + u);
+        // a part that saw nothing, or whose weight vanishes, adds nothing
+        if (c != 0.f)
+#pragma unroll
+          for (int e = 0; e < PER; ++e) acc[e] = fmaf(c, v[u][e], acc[e]);
+      }
     }
-    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-    x *= a.scale;
-    any = true;
-    const float mn = fmaxf(m, x);
-    const float c = m == -INFINITY ? 0.f : expf(m - mn), p = expf(x - mn);
-    m = mn;
-    l = fmaf(l, c, p);
-    for (int e = 0; e < PER; ++e) acc[e] = fmaf(acc[e], c, p * v[e]);
   }
-  for (int e = 0; e < PER; ++e)
-    a.out[row + lane + 32 * e] = f32_to_bf16(any ? acc[e] / l : 0.f);
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  uint16_t *o = a.out + ((size_t)(i.q0 + r / G) * a.q_heads + it.y * G + r % G) * D + lane * PER;
+  if constexpr (PER == 4)
+    *reinterpret_cast<uint2 *>(o) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv),
+                                               pack_bf16(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<uint32_t *>(o) = pack_bf16(acc[0] * inv, acc[1] * inv);
 }
 
-size_t tree_workspace(int q_heads, int kv_heads, int head_dim, int max_query_len) {
-  const int64_t rows = (int64_t)max_query_len * (q_heads / kv_heads);
-  const int64_t ctas = 2 * device_sm_count() + (rows + 127) / 128;
-  return (size_t)(ctas * 2 * 128 * (head_dim + 2) * 4 + 256);
+// Workspace: join records, then the parts' log-sum-exps and outputs.
+struct TreeWorkspace {
+  int64_t ctas;
+  size_t lse_off, o_off, total;
+};
+TreeWorkspace tree_workspace(int group, int head_dim, int max_query_len) {
+  TreeWorkspace w;
+  const int64_t tiles = ((int64_t)max_query_len * group + kTileRows - 1) / kTileRows;
+  w.ctas = 2 * device_sm_count() + (tiles < kMaxRowTiles ? tiles : kMaxRowTiles);
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  w.lse_off = up(w.ctas * sizeof(int4));
+  w.o_off = up(w.lse_off + w.ctas * 2 * kTileRows * sizeof(float));
+  w.total = up(w.o_off + w.ctas * 2 * kTileRows * (size_t)head_dim * sizeof(float));
+  return w;
+}
+
+template <int D, bool F8>
+int launch_tree(TreeArgs a, int64_t tiles, int64_t ctas, const CUtensorMap &tk,
+                const CUtensorMap &tv, cudaStream_t st) {
+  using Lay = TreeLayout<D, F8>;
+  static std::atomic<int> ready[kMaxDevices];  // shared-memory opt-in and carve-out, per device
+  const int r = per_device_setup(ready, [] {
+    cudaError_t e = cudaFuncSetAttribute(tree_attention_kernel<D, F8>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Lay::kSmemLaunch);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(tree_attention_kernel<D, F8>,
+                               cudaFuncAttributePreferredSharedMemoryCarveout,
+                               (int)cudaSharedmemCarveoutMaxShared);
+    return e == cudaSuccess ? 1 : -1;
+  });
+  if (r <= 0) return PKV_ERR_CUDA;
+  a.runs = 2 * device_sm_count();
+  for (int64_t m0 = 0; m0 < tiles; m0 += kMaxRowTiles) {
+    a.m0 = (int)m0;
+    a.row_tiles = (int)(tiles - m0 < kMaxRowTiles ? tiles - m0 : kMaxRowTiles);
+    const unsigned grid = (unsigned)(a.runs + a.row_tiles - 1);
+    if ((int64_t)grid > ctas) return PKV_ERR_WORKSPACE;
+    if (launch_pdl(tree_attention_kernel<D, F8>, dim3(grid), dim3(kTreeThreads),
+                   (size_t)Lay::kSmemLaunch, st, a, tk, tv) != cudaSuccess ||
+        launch_pdl(tree_merge_kernel<D>, dim3(grid, kTileRows / kMergeWarps),
+                   dim3(kMergeWarps * 32), 0, st, a) != cudaSuccess)
+      return PKV_ERR_CUDA;
+  }
+  return PKV_OK;
 }
 
 int tree_impl(uint16_t *out, const uint16_t *q, const void *k_cache, const void *v_cache,
@@ -136,29 +1008,36 @@ int tree_impl(uint16_t *out, const uint16_t *q, const void *k_cache, const void 
   if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return PKV_ERR_ALIGN;
-  if (workspace_bytes < tree_workspace(num_q_heads, num_kv_heads, head_dim, max_query_len))
-    return PKV_ERR_WORKSPACE;
-  TreeArgs a;
+  const int group = num_q_heads / num_kv_heads;
+  const TreeWorkspace ws = tree_workspace(group, head_dim, max_query_len);
+  if (workspace_bytes < ws.total) return PKV_ERR_WORKSPACE;
+  TreeArgs a = {};
   a.out = out, a.q = q, a.k_cache = k_cache, a.v_cache = v_cache;
   a.block_tables = block_tables, a.context_lens = context_lens, a.query_start = query_start;
   a.masks = masks;
   a.num_seqs = num_seqs, a.num_tokens = num_tokens, a.max_blocks = max_blocks_per_seq;
-  a.q_heads = num_q_heads, a.kv_heads = num_kv_heads, a.group = num_q_heads / num_kv_heads;
+  a.q_heads = num_q_heads, a.kv_heads = num_kv_heads, a.group = group;
   a.num_blocks = num_blocks, a.words = mask_words, a.max_query_len = max_query_len;
-  a.scale = scale, a.k_scale = k_scale, a.v_scale = v_scale;
+  a.scale_log2 = (float)((double)scale * (double)k_scale * 1.4426950408889634);
+  a.v_scale = v_scale;
   a.k_scales = k_scales, a.v_scales = v_scales;
+  char *wb = static_cast<char *>(workspace);
+  a.join = reinterpret_cast<int4 *>(wb);
+  a.part_lse = reinterpret_cast<float *>(wb + ws.lse_off);
+  a.part_o = reinterpret_cast<float *>(wb + ws.o_off);
   a.err = err_flag;
-  const dim3 grid((unsigned)(((int64_t)max_query_len * num_q_heads + 7) / 8), 1,
-                  (unsigned)num_seqs);
+  CUtensorMap tk = {}, tv = {};
+  const uint64_t rows = (uint64_t)num_blocks * num_kv_heads * kBlockSize;
+  if (!f8 && (!kv_tensor_map(&tk, k_cache, rows, head_dim, 2) ||
+              !kv_tensor_map(&tv, v_cache, rows, head_dim, 2)))
+    return PKV_ERR_CUDA;
+  const int64_t tiles = ((int64_t)max_query_len * group + kTileRows - 1) / kTileRows;
   const cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t e;
   if (head_dim == 128)
-    e = f8 ? launch_pdl(tree_simple_kernel<128, true>, grid, dim3(256), 0, st, a)
-           : launch_pdl(tree_simple_kernel<128, false>, grid, dim3(256), 0, st, a);
-  else
-    e = f8 ? launch_pdl(tree_simple_kernel<64, true>, grid, dim3(256), 0, st, a)
-           : launch_pdl(tree_simple_kernel<64, false>, grid, dim3(256), 0, st, a);
-  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    return f8 ? launch_tree<128, true>(a, tiles, ws.ctas, tk, tv, st)
+              : launch_tree<128, false>(a, tiles, ws.ctas, tk, tv, st);
+  return f8 ? launch_tree<64, true>(a, tiles, ws.ctas, tk, tv, st)
+            : launch_tree<64, false>(a, tiles, ws.ctas, tk, tv, st);
 }
 
 }  // namespace
@@ -173,7 +1052,7 @@ size_t paged_attention_tree_workspace_size(int num_q_heads, int num_kv_heads, in
   if (num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
       head_dim <= 0 || max_query_len < 0)
     return 0;
-  return tree_workspace(num_q_heads, num_kv_heads, head_dim, max_query_len);
+  return tree_workspace(num_q_heads / num_kv_heads, head_dim, max_query_len).total;
 }
 
 int paged_attention_tree(uint16_t *out, const uint16_t *q, const uint16_t *k_cache,
