@@ -440,8 +440,9 @@ int paged_attention_tree(uint16_t *out, const uint16_t *q, const uint16_t *k_cac
                          float scale, int max_query_len, void *workspace,
                          size_t workspace_bytes, int32_t *err_flag, void *stream);
 
-/* The same over E4M3 caches (q and the weights enter the products as f16, as in
- * paged_attention_decode_fp8).  Scales as in paged_decode_step_fp8; a per-head scale that is
+/* The same over E4M3 caches (q enters the score product as the sum of two E4M3 terms under a
+ * power of two per row, exact for elements down to 2^-9 of the row's largest; the weights
+ * enter theirs as f16).  Scales as in paged_decode_step_fp8; a per-head scale that is
  * not > 0 sets PKV_DEV_BAD_SCALE and the rows reading that head are unspecified. */
 int paged_attention_tree_fp8(uint16_t *out, const uint16_t *q, const uint8_t *k_cache,
                              const uint8_t *v_cache, const int32_t *block_tables,

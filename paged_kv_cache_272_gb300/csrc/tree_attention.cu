@@ -16,9 +16,10 @@
 //    rows are all past the tree only keeps the barriers going.
 //  * warp 4 issues S = Q K^T, warp 7 O += P V (one lane each; issuing takes longer than the
 //    product runs, so neither waits behind the other).
-//  * warps 5 and 6 fill the K and the V ring: TMA tiled copies of the blocks the table names
-//    (bf16), or bulk copies of the E4M3 codes that the warp then widens to f16 (exact) into
-//    the ring.
+//  * warps 5 and 6 fill the K and the V ring with TMA copies of the blocks the table names.
+//    E4M3 cache: K's codes are an operand as they are (q as the sum of two E4M3 terms); V's
+//    go through warps 8-11, which widen them to f16, exactly, because the weights need f16's
+//    range.
 //
 // Split.  With few rows the work is reading the cache, and a batch may be one long sequence
 // or many short ones.  So the key tiles of all (sequence, KV head) pairs of a row tile are
@@ -54,7 +55,12 @@ constexpr unsigned kFullMask = 0xffffffffu;
 constexpr int kTileRows = 128;
 constexpr int kTileKeys = 64;
 constexpr int kTileBlocks = kTileKeys / kBlockSize;
-constexpr int kTreeThreads = 256;
+// Threads per CTA: warps 0-3 softmax, 4-7 products and copies, 8-11 (E4M3) widening.
+__host__ __device__ constexpr int tree_threads(bool f8) { return f8 ? 384 : 256; }
+// E4M3: 384 threads of 80 registers, twice per SM; the softmax warps take 128 and the others
+// leave 56 (128 x 128 + 256 x 56 = 384 x 80).
+constexpr int kLaunchRegs = 80, kSoftmaxRegs = 128, kOtherRegs = 56;
+static_assert(128 * kSoftmaxRegs + 256 * kOtherRegs <= 384 * kLaunchRegs, "register split");
 constexpr uint32_t kTmemColumns = 256;
 constexpr int kMaxRowTiles = 64;  // row tiles of one launch
 constexpr int kMinRun = 1;        // least key tiles per CTA
@@ -106,7 +112,7 @@ __device__ __forceinline__ SeqInfo seq_info(const TreeArgs &a, int s, bool flag)
 // A CTA's run of key tiles, filled by plan_run.
 struct Plan {
   unsigned long long tiles[kMaxRowTiles];  // key tiles of row tile m (all KV heads)
-  unsigned long long warp_sum[kTreeThreads / 32];
+  unsigned long long warp_sum[tree_threads(true) / 32];
   unsigned long long off;  // first tile within sequence s (KV heads end to end)
   long long left;          // tiles of the run
   long long cta_tiles, extra;  // run length of this row tile's CTAs: cta_tiles, one more for
@@ -115,13 +121,14 @@ struct Plan {
 };
 
 // Which key tiles this CTA runs (all threads; the result in *p after the last barrier).
-__device__ void plan_run(const TreeArgs &a, Plan *p) {
+template <int kThreads>
+__device__ __forceinline__ void plan_run(const TreeArgs &a, Plan *p) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid < kMaxRowTiles) p->tiles[tid] = 0;
   if (tid == 0) p->left = 0;
   __syncthreads();
   unsigned long long mine = 0;  // of the last row tile of each sequence, one row tile only
-  for (int s = tid; s < a.num_seqs; s += kTreeThreads) {
+  for (int s = tid; s < a.num_seqs; s += kThreads) {
     const SeqInfo i = seq_info(a, s, blockIdx.x == 0);
     const int last = min(i.row_tiles - a.m0, a.row_tiles);
     if (i.tiles == 0 || last <= 0) continue;
@@ -169,7 +176,7 @@ __device__ void plan_run(const TreeArgs &a, Plan *p) {
   const unsigned long long u0 = p->off;
   const int m = p->m;
   unsigned long long base = 0;
-  for (int s0 = 0; s0 < a.num_seqs; s0 += kTreeThreads) {
+  for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) {
     __syncthreads();
     const int s = s0 + tid;
     unsigned long long n = 0;
@@ -186,7 +193,7 @@ __device__ void plan_run(const TreeArgs &a, Plan *p) {
     if (lane == 31) p->warp_sum[warp] = incl;
     __syncthreads();
     unsigned long long before = base, all = base;
-    for (int w = 0; w < kTreeThreads / 32; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) before += p->warp_sum[w];
       all += p->warp_sum[w];
     }
@@ -238,23 +245,24 @@ struct Walk {
   }
 };
 
-// Shared memory of one CTA (two per SM).  D: head dim; NS: ring slots; F8: E4M3 cache, with
-// RS slots of staged codes.
+// Shared memory of one CTA (two per SM).  D: head dim; F8: E4M3 cache.
 template <int D, bool F8>
 struct TreeLayout {
-  static constexpr int NS = F8 && D == 128 ? 2 : 3;
-  static constexpr int RS = F8 ? 2 : 0;
   static constexpr int kHalves = D / 64;
-  static constexpr int kHalf = kTileKeys * 128;       // 64 keys x 64 columns of 2 bytes
-  static constexpr int kSlot = kHalves * kHalf;
-  static constexpr int kRaw = kTileKeys * D;          // a tile of codes
-  static constexpr int kQ = 0;                        // Q's columns 64..127
+  static constexpr int kHalf = kTileKeys * 128;           // 64 keys x 64 columns of 2 bytes
+  static constexpr int kRaw = kTileKeys * D;              // a tile of codes
+  static constexpr int KS = F8 ? 4 : 3;                   // K ring
+  static constexpr int kKSlot = F8 ? kRaw : kHalves * kHalf;
+  static constexpr int VS = F8 && D == 128 ? 2 : 3;       // V ring (f16 values of an E4M3 cache)
+  static constexpr int kVSlot = kHalves * kHalf;
+  static constexpr int RS = F8 ? 4 : 0;                   // V codes on their way to the V ring
+  // What of Q is not in TMEM: bf16 its columns 64..127, E4M3 (D 128) its second term.
+  static constexpr int kQ = 0;
   static constexpr int kK = (kHalves - 1) * kTileRows * 128;
-  static constexpr int kV = kK + NS * kSlot;
-  static constexpr int kRawK = kV + NS * kSlot;
-  static constexpr int kRawV = kRawK + RS * kRaw;
+  static constexpr int kV = kK + KS * kKSlot;
+  static constexpr int kRawV = kV + VS * kVSlot;
   static constexpr int kBars = kRawV + RS * kRaw;
-  static constexpr int kNumBars = 4 * NS + 7 + 2 * RS;
+  static constexpr int kNumBars = 2 * KS + 2 * VS + 7 + 2 * RS;
   static constexpr int kMisc = kBars + kNumBars * 8;  // TMEM address, abort flag, V marks
   static constexpr int kPlan = kMisc + 96;
   static constexpr int kSmem = kPlan + (int)sizeof(Plan);
@@ -267,8 +275,17 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t *>(&h);
 }
-__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
-  return pack_f16(bf16_lo(w), bf16_hi(w));
+// Four values -> their E4M3 codes, and what is left of the values.
+__device__ __forceinline__ uint32_t e4m3_split(float (&x)[4]) {
+  uint32_t c[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    c[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i], x[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+    const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c[i], __NV_E4M3));
+    x[2 * i] -= __low2float(h);
+    x[2 * i + 1] -= __high2float(h);
+  }
+  return (c[0] & 0xffffu) | (c[1] << 16);
 }
 // Two E4M3 codes (low 16 bits) -> two f16, exact.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t c) {
@@ -297,12 +314,45 @@ __device__ __forceinline__ uint64_t visible_bits(const uint64_t *mask, int t0, i
   return end >= 64 ? b : b & ((1ull << end) - 1);
 }
 
+// The values that were taken out of a row's products because they are not finite, added to
+// the row's stored result (bf16 or fp32) where the row sees them.
 template <int D, bool F8>
-__global__ void __launch_bounds__(kTreeThreads, 2)
+__device__ __noinline__ void add_odd_values(const TreeArgs &a, const Segment &seg,
+                                            const uint64_t *mask, uint32_t tiles, uint16_t *out,
+                                            float *part) {
+  const int first = seg.ctx - seg.L;
+#pragma unroll 1
+  for (; tiles; tiles &= tiles - 1) {
+    const int t0 = (first / kTileKeys + __ffs(tiles) - 1) * kTileKeys;
+    uint64_t see = visible_bits(mask, t0, first, seg.L);
+    if (t0 < first) see &= ~((1ull << (first - t0)) - 1);
+#pragma unroll 1
+    for (; see; see &= see - 1) {
+      const int key = t0 + __ffsll((long long)see) - 1, at = key % kBlockSize;
+      const int blk = a.block_tables[(size_t)seg.s * a.max_blocks + key / kBlockSize];
+      if ((unsigned)blk >= (unsigned)a.num_blocks) continue;
+      const size_t tile = ((size_t)blk * a.kv_heads + seg.g) * (kBlockSize * D);
+#pragma unroll 1
+      for (int d = 0; d < D; ++d) {
+        const float v =
+            F8 ? e4m3_to_f32(static_cast<const uint8_t *>(a.v_cache)[tile + d * kBlockSize + at])
+               : bf16_to_f32(static_cast<const uint16_t *>(a.v_cache)[tile + at * D + d]);
+        if (fabsf(v) < INFINITY) continue;
+        if (out)
+          out[d] = f32_to_bf16(bf16_to_f32(out[d]) + v);
+        else
+          part[d] += v;
+      }
+    }
+  }
+}
+
+template <int D, bool F8>
+__global__ void __launch_bounds__(tree_threads(F8), 2)
     tree_attention_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap tk,
                           const __grid_constant__ CUtensorMap tv) {
   using Lay = TreeLayout<D, F8>;
-  constexpr int H = Lay::kHalves, NS = Lay::NS, RS = Lay::RS;
+  constexpr int H = Lay::kHalves, KS = Lay::KS, VS = Lay::VS, RS = Lay::RS;
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t base = smem_u32(smem);
   if (base & 1023u) {  // the swizzled tiles need a 1024-byte aligned window
@@ -310,26 +360,28 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     return;
   }
   const uint32_t sQ = base + Lay::kQ, sK = base + Lay::kK, sV = base + Lay::kV;
-  const uint32_t k_full = base + Lay::kBars, k_empty = k_full + 8 * NS;
-  const uint32_t v_full = k_empty + 8 * NS, v_empty = v_full + 8 * NS;
-  const uint32_t s_full = v_empty + 8 * NS, s_free = s_full + 8, p_full = s_free + 8;
+  const uint32_t k_full = base + Lay::kBars, k_empty = k_full + 8 * KS;
+  const uint32_t v_full = k_empty + 8 * KS, v_empty = v_full + 8 * VS;
+  const uint32_t s_full = v_empty + 8 * VS, s_free = s_full + 8, p_full = s_free + 8;
   const uint32_t o_done = p_full + 8, fin_s = o_done + 8, fin_o = fin_s + 8;
-  const uint32_t q_full = fin_o + 8, rk_full = q_full + 8, rv_full = rk_full + 8 * RS;
+  const uint32_t q_full = fin_o + 8, raw_full = q_full + 8, raw_empty = raw_full + 8 * RS;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Lay::kMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  // Marks of V tiles that held a value not finite.  E4M3: [ring slot], set by the V warp for
-  // the slot's tile.  bf16: [tile of the tree], the number of the segment that found one.
+  // Marks of V tiles that held a value not finite.  E4M3: [ring slot], 1 + the number of the
+  // CTA's tile that had one.  bf16: [tile of the tree], the number of the segment that did.
   volatile int *v_bad = abort_flag + 1;
-  constexpr int kMarks = F8 ? NS : PKV_TREE_MAX_TOKENS / kTileKeys + 1;
+  constexpr int kMarks = F8 ? VS : PKV_TREE_MAX_TOKENS / kTileKeys + 1;
   static_assert(8 + 4 * kMarks <= 96, "marks");
   Plan *plan = reinterpret_cast<Plan *>(smem + Lay::kPlan);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(k_full + 8 * i, F8 ? 1 : kTileBlocks);
+    for (int i = 0; i < KS; ++i) {
+      mbar_init(k_full + 8 * i, kTileBlocks);
       mbar_init(k_empty + 8 * i, 1);
-      mbar_init(v_full + 8 * i, F8 ? 1 : kTileBlocks);
+    }
+    for (int i = 0; i < VS; ++i) {
+      mbar_init(v_full + 8 * i, kTileBlocks);  // E4M3: one per widening warp
       mbar_init(v_empty + 8 * i, 1);
     }
     mbar_init(s_full, 1);
@@ -340,8 +392,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     mbar_init(fin_o, 1);
     mbar_init(q_full, 4);
     for (int i = 0; i < RS; ++i) {
-      mbar_init(rk_full + 8 * i, kTileBlocks);
-      mbar_init(rv_full + 8 * i, kTileBlocks);
+      mbar_init(raw_full + 8 * i, kTileBlocks);
+      mbar_init(raw_empty + 8 * i, 4);
     }
     *abort_flag = 0;
     for (int i = 0; i < kMarks; ++i) v_bad[i] = 0;
@@ -349,7 +401,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   }
   pdl_trigger();
   pdl_wait();
-  plan_run(a, plan);
+  plan_run<tree_threads(F8)>(a, plan);
   if (plan->left == 0) {
     if (threadIdx.x == 0) a.join[blockIdx.x] = make_int4(0, 0, 0, 0);
     return;
@@ -365,6 +417,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   Segment seg;
 
   if (warp < 4) {
+    if constexpr (F8) set_regs_up<kSoftmaxRegs>();
     // ---------------- softmax warps: thread t owns row t ----------------
     const int t = threadIdx.x;
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
@@ -380,31 +433,73 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       const int i = (valid ? r : rows - 1) / G, first = seg.ctx - seg.L;
       const size_t row = ((size_t)(seg.q0 + i) * a.q_heads + seg.g * G + r % G) * D;
       const uint64_t *mask = a.masks + (size_t)(seg.q0 + i) * a.words;
-      float sl = a.scale_log2, vs = a.v_scale;
+      float sl = a.scale_log2;
+      float vs = a.v_scale;
       if (F8 && a.k_scales != nullptr) {
         const float ks = a.k_scales[seg.g];
         vs = a.v_scales[seg.g];
         if (t == 0 && !(ks > 0.f && vs > 0.f)) flag_error(a.err, PKV_DEV_BAD_SCALE);
         sl *= ks;
       }
-      {
-        // Q: columns 0..63 to TMEM (two 16-bit elements per column), 64..127 to shared memory
-        const uint4 *qrow = reinterpret_cast<const uint4 *>(a.q + row);
-        uint32_t qt[32];
+      const uint4 *qrow = reinterpret_cast<const uint4 *>(a.q + row);
+      if constexpr (!F8) {
+        // columns 0..63 to TMEM (two 16-bit elements per column), 64..127 to shared memory
+#pragma unroll 1
+        for (int half = 0; half < H; ++half) {
+          uint4 v[8];
 #pragma unroll
-        for (int c = 0; c < 8 * H; ++c) {
-          uint4 v = valid ? qrow[c] : make_uint4(0u, 0u, 0u, 0u);
-          if (F8)
-            v = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z),
-                           bf16x2_to_f16x2(v.w));
-          if (c < 8)
-            qt[4 * c] = v.x, qt[4 * c + 1] = v.y, qt[4 * c + 2] = v.z, qt[4 * c + 3] = v.w;
+          for (int c = 0; c < 8; ++c) v[c] = valid ? qrow[8 * half + c] : make_uint4(0u, 0u, 0u, 0u);
+          if (half == 0)
+            tmem_st32(tQ + lane_base, reinterpret_cast<uint32_t (&)[32]>(v));
           else
-            st_shared_v4(sQ + t * 128 + (((c & 7) ^ (t & 7)) << 4), v);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) st_shared_v4(sQ + t * 128 + ((c ^ (t & 7)) << 4), v[c]);
         }
-        tmem_st32(tQ + lane_base, qt);
-        wait_st();
+      } else {
+        // The score product is one of E4M3 with E4M3, so that K's codes enter it as they lie
+        // in the cache.  q is the sum of two E4M3 terms, q 2^e = q1 + q2, e putting the row's
+        // largest element in [128, 256): q1 takes 4 significant bits and q2 the other 4 of
+        // bf16's 8, exactly for elements down to 2^-9 of the largest, and to 2^-10 absolute
+        // below.  q1 goes to TMEM (four codes per column), q2 to shared memory (D 64: TMEM).
+        uint32_t big = 0;  // largest magnitude, as bf16 bits
+#pragma unroll 1
+        for (int half = 0; half < H; ++half) {
+          uint4 v[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) v[c] = valid ? qrow[8 * half + c] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            big = __vmaxu2(big, __vmaxu2(v[c].x & 0x7fff7fffu, v[c].y & 0x7fff7fffu));
+            big = __vmaxu2(big, __vmaxu2(v[c].z & 0x7fff7fffu, v[c].w & 0x7fff7fffu));
+          }
+        }
+        const int bits = max(big & 0xffffu, big >> 16);
+        const bool odd = bits >= 0x7f80;  // an infinity or NaN: no finite score in this row
+        const int e = odd || bits == 0 ? 0 : min(134 - (bits >> 7), 120);
+        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+        sl *= __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll 1
+        for (int c = 0; c < 4 * H; ++c) {  // 16 elements
+          uint32_t q1[4], q2[4];
+          const uint4 v0 = valid ? qrow[2 * c] : make_uint4(0u, 0u, 0u, 0u);
+          const uint4 v1 = valid ? qrow[2 * c + 1] : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            float x[4] = {bf16_lo(w[2 * h]) * up, bf16_hi(w[2 * h]) * up,
+                          bf16_lo(w[2 * h + 1]) * up, bf16_hi(w[2 * h + 1]) * up};
+            q1[h] = odd ? ~0u : e4m3_split(x);
+            q2[h] = odd ? ~0u : e4m3_split(x);
+          }
+          tmem_st4(tQ + 4 * c + lane_base, q1);
+          if (H == 1)
+            tmem_st4(tQ + 16 + 4 * c + lane_base, q2);
+          else
+            st_shared_v4(sQ + t * 128 + ((c ^ (t & 7)) << 4),
+                         make_uint4(q2[0], q2[1], q2[2], q2[3]));
+        }
       }
+      wait_st();
       fence_proxy_async();
       fence_before();
       __syncwarp();
@@ -436,7 +531,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(s_free);  // the next score product may overwrite S
-          if (in_tree) {
+          if (__builtin_expect(in_tree, 0)) {
 #pragma unroll
             for (int c = 0; c < 64; ++c)
               if (!((bits >> c) & 1)) x[c] = __float_as_uint(-INFINITY);
@@ -456,7 +551,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
             // The reference may lag the maximum by 2^8: weights stay below 2^8 and share one
             // reference with the sum and the output, so only a larger jump rescales those.
             const bool need = mx > m + 8.f;
-            if (__any_sync(kFullMask, need)) {
+            if (__builtin_expect(__any_sync(kFullMask, need), 0)) {
               if (!mbar_wait(o_done, (uint32_t)(jt - 1) & 1u, abort_flag, a.err)) {
                 ok = false;
                 break;
@@ -501,16 +596,16 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         } else {
           if (lane == 0) mbar_arrive(s_free);
         }
-        if (in_tree) {
+        if (__builtin_expect(in_tree, 0)) {
           // keys past the context weigh nothing: their V (whatever it is) becomes zero, and
           // so do values of tree tokens that are not finite (E4M3: done by the V warp)
-          const int slot = jt % NS;
-          if (!mbar_wait(v_full + 8 * slot, (uint32_t)(jt / NS) & 1u, abort_flag, a.err)) {
+          const int slot = jt % VS;
+          if (!mbar_wait(v_full + 8 * slot, (uint32_t)(jt / VS) & 1u, abort_flag, a.err)) {
             ok = false;
             break;
           }
           if (!F8) {
-            const uint32_t vst = sV + slot * Lay::kSlot;
+            const uint32_t vst = sV + slot * Lay::kVSlot;
             for (int e = t; e < kTileKeys * 8 * H; e += 128) {
               const int key = e / (8 * H), rem = e % (8 * H);
               const uint32_t at = vst + (rem >> 3) * Lay::kHalf + key * 128 + (rem & 7) * 16;
@@ -532,7 +627,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
               }
             }
             fence_proxy_async();
-          } else if (v_bad[slot]) {
+          } else if (v_bad[slot] == jt + 1) {
             bad |= 1u << (j - tree_tile);
           }
         }
@@ -573,26 +668,6 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         wait_ld();
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
-        for (uint32_t todo = valid ? bad : 0u; todo; todo &= todo - 1) {
-          // the values taken out of this tile's product, for the rows that see them
-          const int t0 = (tree_tile + __ffs(todo) - 1) * kTileKeys;
-          uint64_t see = visible_bits(mask, t0, first, seg.L);
-          if (t0 < first) see &= ~((1ull << (first - t0)) - 1);
-          for (; see; see &= see - 1) {
-            const int key = t0 + __ffsll((long long)see) - 1;
-            const int blk = a.block_tables[(size_t)seg.s * a.max_blocks + key / kBlockSize];
-            if ((unsigned)blk >= (unsigned)a.num_blocks) continue;
-            const size_t tile = ((size_t)blk * a.kv_heads + seg.g) * (kBlockSize * D);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int d = 32 * cc + e, at = key % kBlockSize;
-              const float v =
-                  F8 ? e4m3_to_f32(static_cast<const uint8_t *>(a.v_cache)[tile + d * kBlockSize + at])
-                     : bf16_to_f32(static_cast<const uint16_t *>(a.v_cache)[tile + at * D + d]);
-              if (!(fabsf(v) < INFINITY)) o[e] = __float_as_uint(__uint_as_float(o[e]) + v);
-            }
-          }
-        }
         if (!valid) continue;
         if (whole) {
           uint4 *dst = reinterpret_cast<uint4 *>(a.out + row + 32 * cc);
@@ -610,6 +685,9 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
             dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
       }
+      if (__builtin_expect(bad != 0 && valid, 0))
+        add_odd_values<D, F8>(a, seg, mask, bad, whole ? a.out + row : nullptr,
+                              whole ? nullptr : a.part_o + part * D);
       if (t == 0 && seg.j0 == 0 && !whole) {
         // the CTAs that run the rest of this pair's key tiles
         int parts = 1;
@@ -619,9 +697,11 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       }
     }
     fence_before();
-  } else if (warp == 4) {
+  } else {
+  if constexpr (F8) set_regs_down<kOtherRegs>();
+  if (warp == 4) {
     // ---------------- S warp: lane 0 issues S = Q K^T ----------------
-    constexpr uint32_t id = idesc(kTileRows, kTileKeys, F8, false);
+    constexpr uint32_t id = F8 ? idesc_e4m3(kTileRows, kTileKeys) : idesc(kTileRows, kTileKeys, false, false);
     int jt = 0, ok = 1;
     for (int nseg = 0; ok && walk.next(seg); ++nseg) {
       if (lane == 0) ok = mbar_spin_wait(q_full, (uint32_t)nseg & 1u, abort_flag, a.err);
@@ -629,22 +709,36 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       if (!ok) break;
       fence_after();
       for (int j = seg.j0; j < seg.j1; ++j, ++jt) {
-        const int sb = jt % NS;
+        const int sb = jt % KS;
         if (lane == 0)
-          ok = mbar_spin_wait(k_full + 8 * sb, (uint32_t)(jt / NS) & 1u, abort_flag, a.err) &&
+          ok = mbar_spin_wait(k_full + 8 * sb, (uint32_t)(jt / KS) & 1u, abort_flag, a.err) &&
                (jt < 1 || mbar_spin_wait(s_free, (uint32_t)(jt - 1) & 1u, abort_flag, a.err));
         ok = __shfl_sync(kFullMask, ok, 0);
         if (!ok) break;
         fence_after();
-        const uint32_t kst = sK + sb * Lay::kSlot;
+        const uint32_t kst = sK + sb * Lay::kKSlot;
         if (lane == 0) {
+          if constexpr (!F8) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t b = desc_sw128(kst + (kk >> 2) * Lay::kHalf + (kk & 3) * 32, 16, 1024);
-            if (kk < 4)
-              mma_ts(tS, tQ + 8 * kk, b, id, kk > 0 ? 1u : 0u);
-            else
-              mma_ss(tS, desc_sw128(sQ + (kk & 3) * 32, 16, 1024), b, id, 1u);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t b = desc_sw128(kst + (kk >> 2) * Lay::kHalf + (kk & 3) * 32, 16, 1024);
+              if (kk < 4)
+                mma_ts(tS, tQ + 8 * kk, b, id, kk > 0 ? 1u : 0u);
+              else
+                mma_ss(tS, desc_sw128(sQ + (kk & 3) * 32, 16, 1024), b, id, 1u);
+            }
+          } else {
+            // rows of 128 codes (128-byte swizzle) or 64 (64-byte), 32 columns a product
+#pragma unroll
+            for (int kk = 0; kk < 2 * D / 32; ++kk) {
+              const int c = kk % (D / 32);
+              const uint64_t b = H == 2 ? desc_sw128(kst + c * 32, 16, 1024)
+                                        : desc_sw64(kst + c * 32, 16, 512);
+              if (H == 1 || kk < D / 32)
+                mma_ts_f8(tS, tQ + 8 * kk, b, id, kk > 0 ? 1u : 0u);
+              else
+                mma_ss_f8(tS, desc_sw128(sQ + c * 32, 16, 1024), b, id, 1u);
+            }
           }
           commit(s_full);
           commit(k_empty + 8 * sb);
@@ -664,14 +758,14 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     int jt = 0, ok = 1;
     while (ok && walk.next(seg)) {
       for (int j = seg.j0; j < seg.j1; ++j, ++jt) {
-        const int sb = jt % NS;
+        const int sb = jt % VS;
         if (lane == 0)
           ok = mbar_spin_wait(p_full, (uint32_t)jt & 1u, abort_flag, a.err) &&
-               mbar_spin_wait(v_full + 8 * sb, (uint32_t)(jt / NS) & 1u, abort_flag, a.err);
+               mbar_spin_wait(v_full + 8 * sb, (uint32_t)(jt / VS) & 1u, abort_flag, a.err);
         ok = __shfl_sync(kFullMask, ok, 0);
         if (!ok) break;
         fence_after();
-        const uint32_t vst = sV + sb * Lay::kSlot;
+        const uint32_t vst = sV + sb * Lay::kVSlot;
         if (lane == 0) {
 #pragma unroll
           for (int k = 0; k < kTileKeys / 16; ++k)
@@ -689,11 +783,9 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     __syncwarp();
     mbar_drain(fin_o, 0);
     fence_before();
-  } else {
-    // ---------------- producer warps: warp 5 K, warp 6 V ----------------
+  } else if (warp < 7) {
+    // ---------------- copying warps: warp 5 K, warp 6 V ----------------
     const bool is_v = warp == 6;
-    const uint32_t full = is_v ? v_full : k_full, empty = is_v ? v_empty : k_empty;
-    const uint32_t ring = is_v ? sV : sK;
     // one row tile: the cache is read once, its L2 lines go first; several: the row tiles of
     // a pair share them
     uint64_t pol;
@@ -701,160 +793,135 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
     else
       asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
-    // The block of key tile j that this lane loads, or -1 (past the context, or not a block).
+    // What this warp copies: tiles into a ring of `slots`, lane b the tile's block b.
+    const int slots = F8 && is_v ? RS : is_v ? VS : KS;
+    const uint32_t full = F8 && is_v ? raw_full : is_v ? v_full : k_full;
+    const uint32_t empty = F8 && is_v ? raw_empty : is_v ? v_empty : k_empty;
+    const uint32_t ring = F8 && is_v ? base + Lay::kRawV : is_v ? sV : sK;
+    Walk ahead(walk);
+    Segment as;
+    bool more = ahead.next(as);
+    int aj = as.j0, issued = 0, slot_in = 0;
+    uint32_t empty_parity = 1;  // of the ring's previous round
+    // The table's entry of key tile j for this lane's block (INT_MIN: past the context).  Read
+    // one tile before it is looked at, so that nothing waits for the load.
     auto block_of = [&](const Segment &g, int j) {
       const int tok = j * kTileKeys + lane * kBlockSize;
-      if (lane >= kTileBlocks || tok >= g.ctx) return -1;
-      const int blk = a.block_tables[(size_t)g.s * a.max_blocks + tok / kBlockSize];
-      if ((unsigned)blk < (unsigned)a.num_blocks) return blk;
-      flag_error(a.err, PKV_DEV_BAD_BLOCK);
-      return -1;
+      if (lane >= kTileBlocks || tok >= g.ctx) return INT_MIN;
+      return a.block_tables[(size_t)g.s * a.max_blocks + tok / kBlockSize];
     };
-    if constexpr (!F8) {
-      const CUtensorMap *map = is_v ? &tv : &tk;
-      int issued = 0;
+    int next_blk = more ? block_of(as, aj) : INT_MIN;
+    // Queues the run's next tile once its slot is free; false: gave up.
+    auto issue = [&]() {
+      int blk = next_blk;
+      const int g = as.g;
+      if (blk != INT_MIN && (unsigned)blk >= (unsigned)a.num_blocks) {
+        flag_error(a.err, PKV_DEV_BAD_BLOCK);
+        blk = INT_MIN;
+      }
+      if (++aj >= as.j1) {
+        more = ahead.next(as);
+        aj = as.j0;
+      }
+      if (more) next_blk = block_of(as, aj);  // one tile ahead
+      if (issued >= slots && !mbar_wait(empty + 8 * slot_in, empty_parity, abort_flag, a.err))
+        return false;
       if (lane < kTileBlocks) {
-        bool more = walk.next(seg);
-        int j = seg.j0;
-        int blk = more ? block_of(seg, j) : -1;
-        while (more) {
-          const int slot = issued % NS, g = seg.g, cur = blk;
-          if (++j >= seg.j1) {
-            more = walk.next(seg);
-            j = seg.j0;
-          }
-          if (more) blk = block_of(seg, j);  // one tile ahead
-          if (issued >= NS && !mbar_wait(empty + 8 * slot, (uint32_t)((issued - NS) / NS) & 1u,
-                                         abort_flag, a.err))
-            break;
-          const uint32_t bar = full + 8 * slot;
-          mbar_arrive_expect_tx(bar, cur >= 0 ? 2048u * H : 0u);
-          if (cur >= 0) {
-            const int row = (cur * a.kv_heads + g) * kBlockSize;
-            const uint32_t dst = ring + slot * Lay::kSlot + lane * 2048;
+        const uint32_t bar = full + 8 * slot_in;
+        mbar_arrive_expect_tx(bar, blk >= 0 ? (uint32_t)(kBlockSize * D * (F8 ? 1 : 2)) : 0u);
+        if (blk >= 0) {
+          const int row = (blk * a.kv_heads + g) * kBlockSize;
+          if constexpr (!F8) {
+            const uint32_t dst = ring + slot_in * Lay::kVSlot + lane * 2048;
 #pragma unroll
             for (int h = 0; h < H; ++h)
-              tma_load_2d_hint(dst + h * Lay::kHalf, map, 64 * h, row, bar, pol);
+              tma_load_2d_hint(dst + h * Lay::kHalf, is_v ? &tv : &tk, 64 * h, row, bar, pol);
+          } else if (is_v) {  // [D][16] codes, contiguous
+            bulk_load_hint(ring + slot_in * Lay::kRaw + lane * (kBlockSize * D),
+                           static_cast<const uint8_t *>(a.v_cache) + (size_t)row * D,
+                           kBlockSize * D, bar, pol);
+          } else {
+            tma_load_2d_hint(ring + slot_in * Lay::kRaw + lane * (kBlockSize * D), &tk, 0, row, bar,
+                             pol);
           }
-          ++issued;
         }
       }
-      __syncwarp();
-      if (lane == 0 && *abort_flag)
-        for (int j = max(0, issued - NS); j < issued; ++j)
-          mbar_drain(full + 8 * (j % NS), (uint32_t)(j / NS) & 1u);
-    } else {
-      const uint8_t *cache = static_cast<const uint8_t *>(is_v ? a.v_cache : a.k_cache);
-      const uint32_t raw = base + (is_v ? Lay::kRawV : Lay::kRawK);
-      const uint32_t raw_full = is_v ? rv_full : rk_full;
-      Walk ahead(walk);
-      Segment as;
-      bool more = ahead.next(as);
-      int aj = as.j0, issued = 0, next_blk = more ? block_of(as, aj) : -1;
-      auto issue = [&]() {  // the next tile's codes into the raw ring
-        if (!more) return;
-        const int blk = next_blk, g = as.g;
-        if (++aj >= as.j1) {
-          more = ahead.next(as);
-          aj = as.j0;
-        }
-        if (more) next_blk = block_of(as, aj);  // one tile ahead
-        if (lane < kTileBlocks) {
-          const uint32_t bar = raw_full + 8 * (issued % RS);
-          mbar_arrive_expect_tx(bar, blk >= 0 ? (uint32_t)(kBlockSize * D) : 0u);
-          if (blk >= 0)
-            bulk_load_hint(raw + (issued % RS) * Lay::kRaw + lane * (kBlockSize * D),
-                           cache + ((size_t)blk * a.kv_heads + g) * (kBlockSize * D),
-                           kBlockSize * D, bar, pol);
-        }
-        ++issued;
-      };
-      for (int i = 0; i < RS; ++i) issue();
-      int jt = 0;
+      ++issued;
+      if (++slot_in == slots) slot_in = 0, empty_parity ^= 1;
+      return true;
+    };
+    if (lane < kTileBlocks)
+      while (more && issue()) {
+      }
+    __syncwarp();
+    if (lane == 0 && *abort_flag)
+      for (int j = max(0, issued - slots); j < issued; ++j)
+        mbar_drain(full + 8 * (j % slots), (uint32_t)(j / slots) & 1u);
+  } else if constexpr (F8) {
+    // ---------------- widening warps ----------------
+    // The V codes [D][16 keys] of each tile to f16, exactly, as a K-major operand [D][64 keys]
+    // (128-byte swizzle), a quarter of the 16-code rows each.
+    {
       bool ok = true;
+      int jt = 0;
       while (ok && walk.next(seg)) {
         const int first = seg.ctx - seg.L;
         for (int j = seg.j0; j < seg.j1; ++j, ++jt) {
-          const int slot = jt % NS, rs = jt % RS, t0 = j * kTileKeys;
+          const int slot = jt % VS, rs = jt % RS, t0 = j * kTileKeys;
           ok = mbar_wait(raw_full + 8 * rs, (uint32_t)(jt / RS) & 1u, abort_flag, a.err) &&
-               (jt < NS || mbar_wait(empty + 8 * slot, (uint32_t)((jt - NS) / NS) & 1u, abort_flag,
-                                     a.err));
+               (jt < VS || mbar_wait(v_empty + 8 * slot, (uint32_t)((jt - VS) / VS) & 1u,
+                                     abort_flag, a.err));
           ok = __all_sync(kFullMask, ok);
           if (!ok) break;
-          const uint32_t src = raw + rs * Lay::kRaw, dst = ring + slot * Lay::kSlot;
-          if (!is_v) {
-            // 16 codes a lane and step -> two 16-byte chunks of the key's swizzled row.  A
-            // quarter warp takes two rows and one 64-column half of each, so that neither the
-            // loads nor the stores meet in a bank.
-#pragma unroll 4
-            for (int it = 0; it < kTileKeys * D / 512; ++it) {
-              const int e = it * 32 + lane;
-              int key, c16;  // key row, 16-code column group
-              if (H == 2) {
-                const int pair = e >> 4, q = e & 15;  // two rows, both halves
-                key = pair * 2 + ((q >> 2) & 1);
-                c16 = (((q >> 3) ^ (q >> 2)) & 1) * 4 + (q & 3);
-              } else {
-                key = e >> 2;
-                c16 = e & 3;
+          // A step: 16 codes a lane, row d of block blk, to two chunks of the operand's row.
+          // The loop stays short: a longer body and the softmax's code do not fit the
+          // instruction cache together.
+          constexpr int kSteps = kTileKeys * D / (16 * 128);
+          const int e0 = (warp - 8) * 32 + lane;
+          const uint32_t src = base + Lay::kRawV + rs * Lay::kRaw + e0 * 16;
+          const uint32_t dst = sV + slot * Lay::kVSlot;
+          bool hit = false;
+          if (__builtin_expect(t0 + kTileKeys > first, 0)) {
+            // a tile of the tree: keys past the context, and values that are not finite,
+            // become zero
+#pragma unroll 1
+            for (int it = 0; it < kSteps; ++it) {
+              uint4 v = ld_shared_v4(src + it * 2048);
+              const int key0 = t0 + (it * 128 + e0) / D * kBlockSize;
+#pragma unroll 1
+              for (int b = 0; b < kBlockSize; ++b) {
+                uint32_t &w = b < 8 ? (b < 4 ? v.x : v.y) : (b < 12 ? v.z : v.w);
+                const uint32_t m = 0x7fu << (8 * (b & 3)), key = key0 + b;
+                const bool nan = (w & m) == m && (int)key >= first && (int)key < seg.ctx;
+                if (nan || (int)key >= seg.ctx) w &= ~(0xffu << (8 * (b & 3)));
+                hit |= nan;
               }
-              const uint4 v = ld_shared_v4(src + key * D + c16 * 16);
-              const uint32_t row = dst + (c16 >> 2) * Lay::kHalf + key * 128;
-              const int c = (c16 & 3) * 2;
-              st_shared_v4(row + (((c) ^ (key & 7)) << 4),
-                           make_uint4(e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16),
-                                      e4m3x2_to_f16x2(v.y), e4m3x2_to_f16x2(v.y >> 16)));
-              st_shared_v4(row + (((c + 1) ^ (key & 7)) << 4),
-                           make_uint4(e4m3x2_to_f16x2(v.z), e4m3x2_to_f16x2(v.z >> 16),
-                                      e4m3x2_to_f16x2(v.w), e4m3x2_to_f16x2(v.w >> 16)));
+              st_shared_v4(src + it * 2048, v);
             }
-          } else {
-            const bool in_tree = t0 + kTileKeys > first;
-            bool hit = false;
-#pragma unroll 4
-            for (int it = 0; it < kTileKeys * D / 512; ++it) {
-              const int e = it * 32 + lane, blk = e / D, d = e % D;  // head-dim row of a block
-              uint4 v = ld_shared_v4(src + e * 16);
-              if (in_tree) {
-                uint32_t *w = &v.x;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  const int key = t0 + blk * kBlockSize + q * 4;
-#pragma unroll
-                  for (int b = 0; b < 4; ++b) {
-                    const uint32_t code = (w[q] >> (8 * b)) & 0x7fu;
-                    if (key + b >= seg.ctx) {
-                      w[q] &= ~(0xffu << (8 * b));
-                    } else if (code == 0x7fu && key + b >= first) {
-                      w[q] &= ~(0xffu << (8 * b));
-                      hit = true;
-                    }
-                  }
-                }
-              }
-              const uint32_t row = dst + d * 128;
-              const int c = blk * 2;
-              st_shared_v4(row + (((c) ^ (d & 7)) << 4),
-                           make_uint4(e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16),
-                                      e4m3x2_to_f16x2(v.y), e4m3x2_to_f16x2(v.y >> 16)));
-              st_shared_v4(row + (((c + 1) ^ (d & 7)) << 4),
-                           make_uint4(e4m3x2_to_f16x2(v.z), e4m3x2_to_f16x2(v.z >> 16),
-                                      e4m3x2_to_f16x2(v.w), e4m3x2_to_f16x2(v.w >> 16)));
-            }
-            const bool any = __any_sync(kFullMask, hit);
-            if (lane == 0) v_bad[slot] = any;  // read by the softmax warps after v_full
           }
+#pragma unroll 2
+          for (int it = 0; it < kSteps; ++it) {
+            const uint4 v = ld_shared_v4(src + it * 2048);
+            const int e = it * 128 + e0, blk = e / D, d = e % D;
+            const uint32_t row = dst + d * 128;
+            st_shared_v4(row + (((blk * 2) ^ (d & 7)) << 4),
+                         make_uint4(e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16),
+                                    e4m3x2_to_f16x2(v.y), e4m3x2_to_f16x2(v.y >> 16)));
+            st_shared_v4(row + (((blk * 2 + 1) ^ (d & 7)) << 4),
+                         make_uint4(e4m3x2_to_f16x2(v.z), e4m3x2_to_f16x2(v.z >> 16),
+                                    e4m3x2_to_f16x2(v.w), e4m3x2_to_f16x2(v.w >> 16)));
+          }
+          if (hit) v_bad[slot] = jt + 1;  // read by the softmax warps after v_full
           fence_proxy_async();
           __syncwarp();
-          if (lane == 0) mbar_arrive(full + 8 * slot);
-          issue();
+          if (lane == 0) {
+            mbar_arrive(raw_empty + 8 * rs);
+            mbar_arrive(v_full + 8 * slot);
+          }
         }
       }
-      __syncwarp();
-      if (lane == 0 && *abort_flag)
-        for (int j = max(0, issued - RS); j < issued; ++j)
-          mbar_drain(raw_full + 8 * (j % RS), (uint32_t)(j / RS) & 1u);
     }
+  }
   }
 
   __syncthreads();
@@ -966,7 +1033,10 @@ int launch_tree(TreeArgs a, int64_t tiles, int64_t ctas, const CUtensorMap &tk,
       e = cudaFuncSetAttribute(tree_attention_kernel<D, F8>,
                                cudaFuncAttributePreferredSharedMemoryCarveout,
                                (int)cudaSharedmemCarveoutMaxShared);
-    return e == cudaSuccess ? 1 : -1;
+    // the register split above draws on what the kernel was compiled for
+    cudaFuncAttributes at;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, tree_attention_kernel<D, F8>);
+    return e == cudaSuccess && (!F8 || at.numRegs >= kLaunchRegs) ? 1 : -1;
   });
   if (r <= 0) return PKV_ERR_CUDA;
   a.runs = 2 * device_sm_count();
@@ -975,7 +1045,7 @@ int launch_tree(TreeArgs a, int64_t tiles, int64_t ctas, const CUtensorMap &tk,
     a.row_tiles = (int)(tiles - m0 < kMaxRowTiles ? tiles - m0 : kMaxRowTiles);
     const unsigned grid = (unsigned)(a.runs + a.row_tiles - 1);
     if ((int64_t)grid > ctas) return PKV_ERR_WORKSPACE;
-    if (launch_pdl(tree_attention_kernel<D, F8>, dim3(grid), dim3(kTreeThreads),
+    if (launch_pdl(tree_attention_kernel<D, F8>, dim3(grid), dim3(tree_threads(F8)),
                    (size_t)Lay::kSmemLaunch, st, a, tk, tv) != cudaSuccess ||
         launch_pdl(tree_merge_kernel<D>, dim3(grid, kTileRows / kMergeWarps),
                    dim3(kMergeWarps * 32), 0, st, a) != cudaSuccess)
@@ -1028,8 +1098,8 @@ int tree_impl(uint16_t *out, const uint16_t *q, const void *k_cache, const void 
   a.err = err_flag;
   CUtensorMap tk = {}, tv = {};
   const uint64_t rows = (uint64_t)num_blocks * num_kv_heads * kBlockSize;
-  if (!f8 && (!kv_tensor_map(&tk, k_cache, rows, head_dim, 2) ||
-              !kv_tensor_map(&tv, v_cache, rows, head_dim, 2)))
+  if (!kv_tensor_map(&tk, k_cache, rows, head_dim, f8 ? 1 : 2) ||
+      (!f8 && !kv_tensor_map(&tv, v_cache, rows, head_dim, 2)))
     return PKV_ERR_CUDA;
   const int64_t tiles = ((int64_t)max_query_len * group + kTileRows - 1) / kTileRows;
   const cudaStream_t st = (cudaStream_t)stream;
