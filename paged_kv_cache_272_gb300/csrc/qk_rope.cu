@@ -29,6 +29,7 @@ constexpr int kMaxAxes = 4;
 constexpr int kMaxPairs = 64;
 constexpr int kRopeThreads = 256;
 constexpr int kMaxTile = 4;  // tokens per CTA
+constexpr int kBatch = 4;    // rows a lane group has in flight
 
 struct RopeArgs {
   uint16_t *q_out;
@@ -61,6 +62,10 @@ __device__ __forceinline__ void unpack8(const uint4 &v, float (&x)[8]) {
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t *>(&v);
+}
+
+__device__ __forceinline__ uint4 ld_row(const uint16_t *p) {
+  return *reinterpret_cast<const uint4 *>(p);
 }
 
 // One group of D / 8 lanes owns a (token, head) row, 8 elements a lane.
@@ -112,90 +117,106 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_write_kernel(const 
     write = false;
   }
   const int rows = a.q_heads + 2 * a.kv_heads;
-  const int r_end = min(rows, ((int)blockIdx.y + 1) * a.chunk);
-  for (int r = blockIdx.y * a.chunk + grp / tile; r < r_end; r += GROUPS / tile) {
-    const bool is_q = r < a.q_heads, is_v = r >= a.q_heads + a.kv_heads;
-    const int h = is_q ? r : is_v ? r - a.q_heads - a.kv_heads : r - a.q_heads;
-    if (!is_q && !write) continue;
-    const uint16_t *src = is_q ? a.q + t * a.q_stride : is_v ? a.v + t * a.v_stride
-                                                             : a.k + t * a.k_stride;
-    const uint4 raw = *reinterpret_cast<const uint4 *>(src + (int64_t)h * D + e * 8);
-    const int64_t row16 = ((slot >> 4) * a.kv_heads + h) * kBlockSize + (slot & 15);
-    float ks = a.k_scale, vs = a.v_scale;
-    if (F8 && !is_q && a.k_scales != nullptr) {
-      ks = a.k_scales[h], vs = a.v_scales[h];
-      if (!(ks > 0.f) || !(vs > 0.f)) {
-        if (e == 0) flag_error(a.err, PKV_DEV_BAD_SCALE);
-        continue;
-      }
-    }
-    if (is_v) {
-      if constexpr (!F8) {
-        reinterpret_cast<uint4 *>(a.v_cache)[row16 * LPR + e] = raw;
-      } else {
-        // transposed block [D][16]: lanes trade codes so a round covers consecutive rows
-        const uint32_t c0 = quant4(raw.x, raw.y, vs), c1 = quant4(raw.z, raw.w, vs);
-        uint8_t *blk = static_cast<uint8_t *>(a.v_cache) +
-                       ((slot >> 4) * a.kv_heads + h) * (int64_t)(D * kBlockSize) + (slot & 15);
+  const int r_end = min(rows, ((int)blockIdx.y + 1) * a.chunk), step = GROUPS / tile;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  const uint4 qw = a.q_weight ? *reinterpret_cast<const uint4 *>(a.q_weight + e * 8) : zero;
+  const uint4 kw = a.k_weight ? *reinterpret_cast<const uint4 *>(a.k_weight + e * 8) : zero;
+  for (int r0 = blockIdx.y * a.chunk + grp / tile; r0 < r_end; r0 += kBatch * step) {
+    uint4 raw[kBatch];  // every load of the batch before the first use
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int d = LPR * k + e;
-          const uint32_t w0 = __shfl_sync(gmask, c0, gbase + (d >> 3));
-          const uint32_t w1 = __shfl_sync(gmask, c1, gbase + (d >> 3));
-          blk[d * kBlockSize] = (uint8_t)(((d & 4) ? w1 : w0) >> (8 * (d & 3)));
+    for (int u = 0; u < kBatch; ++u) {
+      const int r = r0 + u * step;
+      raw[u] = zero;
+      if (r < a.q_heads)
+        raw[u] = ld_row(a.q + t * a.q_stride + (int64_t)r * D + e * 8);
+      else if (r < r_end && write)
+        raw[u] = r < a.q_heads + a.kv_heads
+                     ? ld_row(a.k + t * a.k_stride + (int64_t)(r - a.q_heads) * D + e * 8)
+                     : ld_row(a.v + t * a.v_stride +
+                              (int64_t)(r - a.q_heads - a.kv_heads) * D + e * 8);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int r = r0 + u * step;
+      const bool is_q = r < a.q_heads, is_v = r >= a.q_heads + a.kv_heads;
+      if (r >= r_end || (!is_q && !write)) continue;
+      const int h = is_q ? r : is_v ? r - a.q_heads - a.kv_heads : r - a.q_heads;
+      const int64_t row16 = ((slot >> 4) * a.kv_heads + h) * kBlockSize + (slot & 15);
+      float ks = a.k_scale, vs = a.v_scale;
+      if (F8 && !is_q && a.k_scales != nullptr) {
+        ks = a.k_scales[h], vs = a.v_scales[h];
+        if (!(ks > 0.f) || !(vs > 0.f)) {
+          if (e == 0) flag_error(a.err, PKV_DEV_BAD_SCALE);
+          continue;
         }
       }
-      continue;
-    }
-    float x[8];
-    unpack8(raw, x);
-    const uint16_t *wt = is_q ? a.q_weight : a.k_weight;
-    if (wt != nullptr) {
-      float ss = 0.f;
+      if (is_v) {
+        if constexpr (!F8) {
+          reinterpret_cast<uint4 *>(a.v_cache)[row16 * LPR + e] = raw[u];
+        } else {
+          // transposed block [D][16]: lanes trade codes so a round covers consecutive rows
+          const uint32_t c0 = quant4(raw[u].x, raw[u].y, vs), c1 = quant4(raw[u].z, raw[u].w, vs);
+          uint8_t *blk = static_cast<uint8_t *>(a.v_cache) +
+                         ((slot >> 4) * a.kv_heads + h) * (int64_t)(D * kBlockSize) + (slot & 15);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-#pragma unroll
-      for (int off = LPR / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(gmask, ss, off);
-      const float inv = rsqrtf(fmaf(ss, 1.0f / D, a.eps));
-      float w[8];
-      unpack8(*reinterpret_cast<const uint4 *>(wt + e * 8), w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = x[j] * inv * w[j];
-    }
-    float y[8];
-    if (a.interleaved) {
-#pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        y[j] = x[j] * cs[j] - x[j + 1] * sn[j];
-        y[j + 1] = x[j + 1] * cs[j] + x[j] * sn[j];
+          for (int k = 0; k < 8; ++k) {
+            const int d = LPR * k + e;
+            const uint32_t w0 = __shfl_sync(gmask, c0, gbase + (d >> 3));
+            const uint32_t w1 = __shfl_sync(gmask, c1, gbase + (d >> 3));
+            blk[d * kBlockSize] = (uint8_t)(((d & 4) ? w1 : w0) >> (8 * (d & 3)));
+          }
+        }
+        continue;
       }
-    } else {
+      float x[8];
+      unpack8(raw[u], x);
+      if ((is_q ? a.q_weight : a.k_weight) != nullptr) {
+        float ss = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float o = __shfl_sync(gmask, x[j], partner);
-        y[j] = x[j] * cs[j] + (second ? o : -o) * sn[j];
+        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+#pragma unroll
+        for (int off = LPR / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(gmask, ss, off);
+        const float inv = rsqrtf(fmaf(ss, 1.0f / D, a.eps));
+        float w[8];
+        unpack8(is_q ? qw : kw, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = x[j] * inv * w[j];
       }
-    }
-    if (!rotates) {
+      float y[8];
+      if (a.interleaved) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = x[j];
-    }
-    if (!F8 || is_q) {
-      const uint4 o = make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]),
-                                 pack2(y[6], y[7]));
-      if (is_q)
-        *reinterpret_cast<uint4 *>(a.q_out + t * a.q_out_stride + (int64_t)h * D + e * 8) = o;
-      else
-        reinterpret_cast<uint4 *>(a.k_cache)[row16 * LPR + e] = o;
-    } else {
-      uint32_t c[4];
+        for (int j = 0; j < 8; j += 2) {
+          y[j] = x[j] * cs[j] - x[j + 1] * sn[j];
+          y[j + 1] = x[j + 1] * cs[j] + x[j] * sn[j];
+        }
+      } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        c[j] = __nv_cvt_float2_to_fp8x2(
-            make_float2(__fdiv_rn(y[2 * j], ks), __fdiv_rn(y[2 * j + 1], ks)), __NV_SATFINITE,
-            __NV_E4M3);
-      reinterpret_cast<uint2 *>(a.k_cache)[row16 * LPR + e] =
-          make_uint2((c[0] & 0xffffu) | (c[1] << 16), (c[2] & 0xffffu) | (c[3] << 16));
+        for (int j = 0; j < 8; ++j) {
+          const float o = __shfl_sync(gmask, x[j], partner);
+          y[j] = x[j] * cs[j] + (second ? o : -o) * sn[j];
+        }
+      }
+      if (!rotates) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = x[j];
+      }
+      if (!F8 || is_q) {
+        const uint4 o = make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]),
+                                   pack2(y[6], y[7]));
+        if (is_q)
+          *reinterpret_cast<uint4 *>(a.q_out + t * a.q_out_stride + (int64_t)h * D + e * 8) = o;
+        else
+          reinterpret_cast<uint4 *>(a.k_cache)[row16 * LPR + e] = o;
+      } else {
+        uint32_t c[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          c[j] = __nv_cvt_float2_to_fp8x2(
+              make_float2(__fdiv_rn(y[2 * j], ks), __fdiv_rn(y[2 * j + 1], ks)), __NV_SATFINITE,
+              __NV_E4M3);
+        reinterpret_cast<uint2 *>(a.k_cache)[row16 * LPR + e] =
+            make_uint2((c[0] & 0xffffu) | (c[1] << 16), (c[2] & 0xffffu) | (c[3] << 16));
+      }
     }
   }
 }
@@ -231,10 +252,17 @@ int rope_impl(RopeArgs &a, const uint8_t *pair_axis, int num_axes, int rotary_di
   a.num_slots = (int64_t)num_blocks * kBlockSize;
   const int rows = a.q_heads + 2 * a.kv_heads;
   const int groups = kRopeThreads * 8 / head_dim;
-  // Many tokens: 4 per CTA, every head (a token's sines are made once).  Few: one token
-  // and one row per lane group, so that a small step spreads over the SMs.
-  a.tile = a.num_tokens >= 16 * device_sm_count() ? kMaxTile : 1;
-  a.chunk = a.tile == 1 ? groups : rows;
+  // Many tokens: 4 per CTA, every head (a token's sines are made once).  Fewer: one token per
+  // CTA, its rows split over CTAs until there are four per SM or a lane group has one row.
+  const int sms = device_sm_count();
+  a.tile = a.num_tokens >= 16 * sms ? kMaxTile : 1;
+  int parts = 1;
+  if (a.tile == 1) {
+    parts = 4 * sms / a.num_tokens;
+    const int most = (rows + groups - 1) / groups;
+    parts = parts < 1 ? 1 : parts > most ? most : parts;
+  }
+  a.chunk = ((rows + parts - 1) / parts + groups - 1) / groups * groups;
   const unsigned ny = (unsigned)((rows + a.chunk - 1) / a.chunk);
   if (ny > 65535) return PKV_ERR_SHAPE;
   const dim3 grid((unsigned)((a.num_tokens + a.tile - 1) / a.tile), ny);

@@ -86,7 +86,7 @@ constexpr int kSlice = 128;         // bytes of a row one CTA moves
 constexpr int kCommitThreads = 128;
 
 __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const CommitArgs a) {
-  extern __shared__ __align__(16) uint8_t stage[];  // [max_accept][kSlice]
+  extern __shared__ __align__(16) uint8_t stage[];  // [max_accept][kSlice], then slot pairs
   pdl_trigger();
   pdl_wait();
   const int s = blockIdx.x, h = blockIdx.y;
@@ -100,21 +100,25 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const Commi
     if (threadIdx.x == 0) flag_error(a.err, PKV_DEV_BAD_CONTEXT);
     return;
   }
-  // Source and destination slots of accepted row r; false: the row is not moved.
-  auto slots_of = [&](int r, int64_t &src, int64_t &dst) {
+  // Source and destination slots of the accepted rows, once per CTA (-1: not moved).
+  int64_t *const ss = reinterpret_cast<int64_t *>(stage + (size_t)a.max_accept * kSlice);
+  for (int r = threadIdx.x; r < n; r += kCommitThreads) {
     const int idx = a.accepted[(size_t)s * a.max_accept + r];
+    int64_t src = -1, dst = -1;
     if (idx < 0 || idx >= L) {
       flag_error(a.err, PKV_DEV_BAD_ROW);
-      return false;
+    } else {
+      src = a.slots[q0 + idx];
+      dst = a.dst_slots ? a.dst_slots[(size_t)s * a.max_accept + r] : a.slots[q0 + r];
+      if (src >= a.num_slots || dst >= a.num_slots) {
+        flag_error(a.err, PKV_DEV_BAD_SLOT);
+        src = -1;
+      }
     }
-    src = a.slots[q0 + idx];
-    dst = a.dst_slots ? a.dst_slots[(size_t)s * a.max_accept + r] : a.slots[q0 + r];
-    if (src >= a.num_slots || dst >= a.num_slots) {
-      flag_error(a.err, PKV_DEV_BAD_SLOT);
-      return false;
-    }
-    return src >= 0 && dst >= 0;
-  };
+    ss[2 * r] = dst < 0 ? -1 : src;
+    ss[2 * r + 1] = dst;
+  }
+  __syncthreads();
   uint8_t *cache = is_v ? a.v_cache : a.k_cache;
   const int64_t row_bytes = (int64_t)a.head_dim * a.elem;
   if (is_v && a.v_transposed) {
@@ -123,14 +127,12 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const Commi
     auto at = [&](int64_t slot) {
       return cache + (((slot >> 4) * a.heads + h) * a.head_dim + d) * kBlockSize + (slot & 15);
     };
-    int64_t src, dst;
-    if (d < a.head_dim)
-      for (int r = 0; r < n; ++r)
-        if (slots_of(r, src, dst)) stage[r * kSlice + d] = *at(src);
-    __syncthreads();
-    if (d < a.head_dim)
-      for (int r = 0; r < n; ++r)
-        if (slots_of(r, src, dst)) *at(dst) = stage[r * kSlice + d];
+    if (d >= a.head_dim) return;  // no thread reads another's bytes
+#pragma unroll 8
+    for (int r = 0; r < n; ++r)
+      if (ss[2 * r] >= 0) stage[r * kSlice + d] = *at(ss[2 * r]);
+    for (int r = 0; r < n; ++r)
+      if (ss[2 * r] >= 0) *at(ss[2 * r + 1]) = stage[r * kSlice + d];
     return;
   }
   const int lanes = row_bytes < kSlice ? (int)(row_bytes / 16) : kSlice / 16;
@@ -141,12 +143,12 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const Commi
         slice * kSlice + e * 16);
   };
   uint4 *st = reinterpret_cast<uint4 *>(stage);
-  int64_t src, dst;
+#pragma unroll 4
   for (int r = threadIdx.x / lanes; r < n; r += step)
-    if (slots_of(r, src, dst)) st[r * (kSlice / 16) + e] = *at(src);
+    if (ss[2 * r] >= 0) st[r * (kSlice / 16) + e] = *at(ss[2 * r]);
   __syncthreads();
   for (int r = threadIdx.x / lanes; r < n; r += step)
-    if (slots_of(r, src, dst)) *at(dst) = st[r * (kSlice / 16) + e];
+    if (ss[2 * r] >= 0) *at(ss[2 * r + 1]) = st[r * (kSlice / 16) + e];
 }
 
 int commit_impl(void *k_cache, void *v_cache, const int64_t *slot_mapping,
@@ -182,7 +184,7 @@ int commit_impl(void *k_cache, void *v_cache, const int64_t *slot_mapping,
   static std::atomic<int> ready[kMaxDevices];
   const int r = per_device_setup(ready, [] {
     return cudaFuncSetAttribute(tree_commit_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                PKV_TREE_MAX_TOKENS * kSlice) == cudaSuccess
+                                PKV_TREE_MAX_TOKENS * (kSlice + 16)) == cudaSuccess
                ? 1
                : -1;
   });
@@ -191,7 +193,7 @@ int commit_impl(void *k_cache, void *v_cache, const int64_t *slot_mapping,
   const cudaError_t e = launch_pdl(
       tree_commit_kernel,
       dim3((unsigned)num_seqs, (unsigned)num_kv_heads, (unsigned)(2 * slices)),
-      dim3(kCommitThreads), (size_t)max_accept * kSlice, (cudaStream_t)stream, a);
+      dim3(kCommitThreads), (size_t)max_accept * (kSlice + 16), (cudaStream_t)stream, a);
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
