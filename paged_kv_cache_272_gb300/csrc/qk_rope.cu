@@ -13,14 +13,20 @@
 // position, however far the position -- where an fp32 product would be 0.06 rad off at a
 // million.  sincospi then takes the top bits.
 //
-// Bound: bytes.  Every row is read once and written once; a token's sines are made once per
-// CTA (kTile tokens share it) and held in registers across the heads a lane serves.
+// Layout: D / 8 lanes own a (token, head) row.  A rotating lane holds four elements of each
+// half (half-split pairs) or four adjacent pairs, so both elements of a pair meet in one lane
+// and nothing is exchanged but the norm's sum; its four sines stay in registers for all the
+// heads it serves.  Two rows are in flight behind the one being worked on.
+//
+// Bound: bytes, with the instruction issue close behind (16 bytes a lane and row), hence the
+// packed arithmetic and the division below.
 #include <math.h>
 
 #include <cstring>
 
 #include "kv_rows.cuh"
 #include "pkv_common.cuh"
+#include "tc_common.cuh"  // packed f32x2 arithmetic
 
 namespace pkv {
 namespace {
@@ -29,7 +35,6 @@ constexpr int kMaxAxes = 4;
 constexpr int kMaxPairs = 64;
 constexpr int kRopeThreads = 256;
 constexpr int kMaxTile = 4;  // tokens per CTA
-constexpr int kBatch = 4;    // rows a lane group has in flight
 
 struct RopeArgs {
   uint16_t *q_out;
@@ -55,22 +60,51 @@ struct RopeArgs {
   uint8_t pair_axis[kMaxPairs];
 };
 
-__device__ __forceinline__ void unpack8(const uint4 &v, float (&x)[8]) {
-  x[0] = bf16_lo(v.x), x[1] = bf16_hi(v.x), x[2] = bf16_lo(v.y), x[3] = bf16_hi(v.y);
-  x[4] = bf16_lo(v.z), x[5] = bf16_hi(v.z), x[6] = bf16_lo(v.w), x[7] = bf16_hi(v.w);
-}
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t *>(&v);
 }
+__device__ __forceinline__ uint64_t bf16x2_to_f32x2(uint32_t w) { return f32x2(bf16_lo(w), bf16_hi(w)); }
 
-__device__ __forceinline__ uint4 ld_row(const uint16_t *p) {
-  return *reinterpret_cast<const uint4 *>(p);
-}
+// x / s rounded to nearest for a whole row by one reciprocal: with y = RN(1 / s), q = RN(x y)
+// and the exact remainder r = x - q s, RN(q + r y) is the rounded quotient (P. Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor", IBM J. Res.
+// Dev. 34, 1990), as long as nothing over- or underflows on the way: a scale within 2^+-60
+// here, and quotients beyond 2^20 keep q (their code is that of the largest value either
+// way); quotients that underflow have code 0.  Other scales divide.
+struct RowDivide {
+  float s, y;
+  bool exact;
+  __device__ explicit RowDivide(float scale) : s(scale), y(1.0f / scale) {
+    exact = scale > 8.7e-19f && scale < 1.1e18f;
+  }
+  __device__ float2 operator()(float a, float b) const {
+    if (!exact) return make_float2(__fdiv_rn(a, s), __fdiv_rn(b, s));
+    const uint64_t x = f32x2(a, b), y2 = f32x2(y, y);
+    const uint64_t q = mul_f32x2(x, y2);
+    const uint64_t r = fma_f32x2(q, f32x2(-s, -s), x);
+    const uint64_t z = fma_f32x2(r, y2, q);
+    float q0, q1, z0, z1;
+    f32x2_split(q, q0, q1);
+    f32x2_split(z, z0, z1);
+    auto pick = [](float big, float quot) {
+      // a zero keeps the sign of the product (the correction's is always +0)
+      const uint32_t z = __float_as_uint(quot) | (__float_as_uint(big) & 0x80000000u);
+      return fabsf(big) > 1048576.f ? big : __uint_as_float(z);
+    };
+    return make_float2(pick(q0, z0), pick(q1, z1));
+  }
+  // Codes of four values, lowest byte first.
+  __device__ uint32_t codes(float a, float b, float c, float d) const {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2((*this)(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2((*this)(c, d), __NV_SATFINITE, __NV_E4M3);
+    return (lo & 0xffffu) | (hi << 16);
+  }
+};
 
-// One group of D / 8 lanes owns a (token, head) row, 8 elements a lane.
-template <int D, bool F8>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_write_kernel(const __grid_constant__ RopeArgs a) {
+template <int D, bool F8, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads, 4)
+    qk_norm_rope_write_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int LPR = D / 8;
   constexpr int GROUPS = kRopeThreads / LPR;
   __shared__ __align__(16) float s_cos[kMaxTile][kMaxPairs], s_sin[kMaxTile][kMaxPairs];
@@ -78,147 +112,185 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_write_kernel(const 
   pdl_wait();
   const int tid = threadIdx.x, tile = a.tile;
   const int64_t t0 = (int64_t)blockIdx.x * tile;
-  for (int i = tid; i < tile * a.pairs; i += kRopeThreads) {
-    const int tt = i / a.pairs, p = i - tt * a.pairs;
-    if (t0 + tt < a.num_tokens) {
-      const double turns = a.inv_freq[p] * 0.15915494309189533577;  // per position
-      const uint64_t frac = (uint64_t)__double2ull_rd((turns - floor(turns)) * 18446744073709551616.0);
-      const int pos = a.positions[a.pair_axis[p] * a.axis_stride + t0 + tt];
-      const int64_t turn = (int64_t)((uint64_t)(int64_t)pos * frac);  // modulo one turn
-      float sn, cs;
-      sincospif((float)((int32_t)(turn >> 32)) * (1.0f / 2147483648.0f), &sn, &cs);
-      s_cos[tt][p] = cs * a.rope_scale;
-      s_sin[tt][p] = sn * a.rope_scale;
-    }
-  }
-  __syncthreads();
   const int e = tid % LPR, grp = tid / LPR;
   const int tt = grp % tile;
   const int64_t t = t0 + tt;
-  if (t >= a.num_tokens) return;
+  const bool on = t < a.num_tokens;
+  // This lane's elements of a q or k row: four from oa, four from ob.
+  const int rot_lanes = a.pairs / 4;  // lanes whose elements rotate
+  const bool rotates = e < rot_lanes;
+  const int oa = INTER || !rotates ? 8 * e : 4 * e;
+  const int ob = INTER || !rotates ? 8 * e + 4 : a.pairs + 4 * e;
+  const int rows = a.q_heads + 2 * a.kv_heads, v_rows = a.q_heads + a.kv_heads;
+  const int r_end = on ? min(rows, ((int)blockIdx.y + 1) * a.chunk) : 0, step = GROUPS / tile;
+  const int r_begin = blockIdx.y * a.chunk + grp / tile;
+  const uint16_t *const q_row = a.q + t * a.q_stride;
+  const uint16_t *const k_row = a.k + t * a.k_stride - (int64_t)a.q_heads * D;
+  const uint16_t *const v_row = a.v + t * a.v_stride - (int64_t)v_rows * D;
+  auto load = [&](int r) {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (r >= r_end) return v;
+    const uint16_t *p = (r < a.q_heads ? q_row : r < v_rows ? k_row : v_row) + r * D;
+    const bool is_v = r >= v_rows;
+    const uint2 lo = *reinterpret_cast<const uint2 *>(p + (is_v ? 8 * e : oa));
+    const uint2 hi = *reinterpret_cast<const uint2 *>(p + (is_v ? 8 * e + 4 : ob));
+    return make_uint4(lo.x, lo.y, hi.x, hi.y);
+  };
+  uint4 next = load(r_begin), after = load(r_begin + step);
+  const int64_t slot = on ? a.slots[t] : -1;
+  auto weights = [&](const uint16_t *w) {  // this lane's, two packed words from oa, two from ob
+    if (w == nullptr) return make_uint4(0u, 0u, 0u, 0u);
+    const uint2 lo = *reinterpret_cast<const uint2 *>(w + oa);
+    const uint2 hi = *reinterpret_cast<const uint2 *>(w + ob);
+    return make_uint4(lo.x, lo.y, hi.x, hi.y);
+  };
+  const uint4 qw = weights(a.q_weight), kw = weights(a.k_weight);
+  for (int i = tid; i < tile * a.pairs; i += kRopeThreads) {
+    const int tok = i / a.pairs, p = i - tok * a.pairs;
+    if (t0 + tok < a.num_tokens) {
+      const double turns = a.inv_freq[p] * 0.15915494309189533577;  // per position
+      const uint64_t frac = (uint64_t)__double2ull_rd((turns - floor(turns)) * 18446744073709551616.0);
+      const int pos = a.positions[a.pair_axis[p] * a.axis_stride + t0 + tok];
+      const int64_t turn = (int64_t)((uint64_t)(int64_t)pos * frac);  // modulo one turn
+      float sn, cs;
+      sincospif((float)((int32_t)(turn >> 32)) * (1.0f / 2147483648.0f), &sn, &cs);
+      s_cos[tok][p] = cs * a.rope_scale;
+      s_sin[tok][p] = sn * a.rope_scale;
+    }
+  }
+  __syncthreads();
+  if (!on) return;
   const unsigned gmask = (LPR == 16 ? 0xffffu : 0xffu) << ((tid & 31) & ~(LPR - 1));
   const int gbase = (tid & 31) & ~(LPR - 1);
-  // this lane's sines: 8 half-split elements share 8 pairs, 8 interleaved ones hold 4
-  const int half_lanes = a.pairs / 8;  // lanes of one half (half-split)
-  const bool rotates = e < 2 * half_lanes;
-  const bool second = e >= half_lanes;
-  float cs[8], sn[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int p = a.interleaved ? 4 * e + (j >> 1) : (second ? e - half_lanes : e) * 8 + j;
-    cs[j] = rotates ? s_cos[tt][p] : 1.f;
-    sn[j] = rotates ? s_sin[tt][p] : 0.f;
+  // pairs 4 e .. 4 e + 3, two at a time
+  uint64_t cs[2] = {f32x2(1.f, 1.f), f32x2(1.f, 1.f)}, sn[2] = {0, 0}, ms[2] = {0, 0};
+  if (rotates) {
+    const float4 c = *reinterpret_cast<const float4 *>(&s_cos[tt][4 * e]);
+    const float4 s = *reinterpret_cast<const float4 *>(&s_sin[tt][4 * e]);
+    cs[0] = f32x2(c.x, c.y), cs[1] = f32x2(c.z, c.w);
+    sn[0] = f32x2(s.x, s.y), sn[1] = f32x2(s.z, s.w);
+    ms[0] = f32x2(-s.x, -s.y), ms[1] = f32x2(-s.z, -s.w);
   }
-  const int partner = gbase + (!rotates ? e : second ? e - half_lanes : e + half_lanes);
-  const int64_t slot = a.slots[t];
   bool write = slot >= 0;
   if (slot >= a.num_slots) {
     if (e == 0) flag_error(a.err, PKV_DEV_BAD_SLOT);
     write = false;
   }
-  const int rows = a.q_heads + 2 * a.kv_heads;
-  const int r_end = min(rows, ((int)blockIdx.y + 1) * a.chunk), step = GROUPS / tile;
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  const uint4 qw = a.q_weight ? *reinterpret_cast<const uint4 *>(a.q_weight + e * 8) : zero;
-  const uint4 kw = a.k_weight ? *reinterpret_cast<const uint4 *>(a.k_weight + e * 8) : zero;
-  for (int r0 = blockIdx.y * a.chunk + grp / tile; r0 < r_end; r0 += kBatch * step) {
-    uint4 raw[kBatch];  // every load of the batch before the first use
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int r = r0 + u * step;
-      raw[u] = zero;
-      if (r < a.q_heads)
-        raw[u] = ld_row(a.q + t * a.q_stride + (int64_t)r * D + e * 8);
-      else if (r < r_end && write)
-        raw[u] = r < a.q_heads + a.kv_heads
-                     ? ld_row(a.k + t * a.k_stride + (int64_t)(r - a.q_heads) * D + e * 8)
-                     : ld_row(a.v + t * a.v_stride +
-                              (int64_t)(r - a.q_heads - a.kv_heads) * D + e * 8);
-    }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int r = r0 + u * step;
-      const bool is_q = r < a.q_heads, is_v = r >= a.q_heads + a.kv_heads;
-      if (r >= r_end || (!is_q && !write)) continue;
-      const int h = is_q ? r : is_v ? r - a.q_heads - a.kv_heads : r - a.q_heads;
-      const int64_t row16 = ((slot >> 4) * a.kv_heads + h) * kBlockSize + (slot & 15);
-      float ks = a.k_scale, vs = a.v_scale;
-      if (F8 && !is_q && a.k_scales != nullptr) {
-        ks = a.k_scales[h], vs = a.v_scales[h];
-        if (!(ks > 0.f) || !(vs > 0.f)) {
+  const int64_t block_row = (slot >> 4) * a.kv_heads;  // of KV head 0
+  const int off = (int)(slot & 15);
+  uint16_t *const q_out = a.q_out + t * a.q_out_stride;
+#pragma unroll 1
+  for (int r = r_begin; r < r_end; r += step) {
+    const uint4 raw = next;
+    next = after;
+    after = load(r + 2 * step);
+    const bool is_q = r < a.q_heads;
+    if (!is_q && !write) continue;
+    if (r >= v_rows) {
+      const int64_t blk = (block_row + (r - v_rows)) * (kBlockSize * D);
+      if constexpr (!F8) {
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.v_cache) + blk + off * D + 8 * e) = raw;
+      } else {
+        const float vs = a.v_scales ? a.v_scales[r - v_rows] : a.v_scale;
+        if (!(vs > 0.f) || (a.k_scales && !(a.k_scales[r - v_rows] > 0.f))) {
           if (e == 0) flag_error(a.err, PKV_DEV_BAD_SCALE);
           continue;
         }
-      }
-      if (is_v) {
-        if constexpr (!F8) {
-          reinterpret_cast<uint4 *>(a.v_cache)[row16 * LPR + e] = raw[u];
-        } else {
-          // transposed block [D][16]: lanes trade codes so a round covers consecutive rows
-          const uint32_t c0 = quant4(raw[u].x, raw[u].y, vs), c1 = quant4(raw[u].z, raw[u].w, vs);
-          uint8_t *blk = static_cast<uint8_t *>(a.v_cache) +
-                         ((slot >> 4) * a.kv_heads + h) * (int64_t)(D * kBlockSize) + (slot & 15);
+        // transposed block [D][16]: lanes trade codes so that a round covers consecutive rows
+        const RowDivide div(vs);
+        const uint32_t c0 = div.codes(bf16_lo(raw.x), bf16_hi(raw.x), bf16_lo(raw.y), bf16_hi(raw.y));
+        const uint32_t c1 = div.codes(bf16_lo(raw.z), bf16_hi(raw.z), bf16_lo(raw.w), bf16_hi(raw.w));
+        uint8_t *dst = static_cast<uint8_t *>(a.v_cache) + blk + e * kBlockSize + off;
+        const uint32_t sh = 8 * (e & 3);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int d = LPR * k + e;
-            const uint32_t w0 = __shfl_sync(gmask, c0, gbase + (d >> 3));
-            const uint32_t w1 = __shfl_sync(gmask, c1, gbase + (d >> 3));
-            blk[d * kBlockSize] = (uint8_t)(((d & 4) ? w1 : w0) >> (8 * (d & 3)));
-          }
+        for (int k = 0; k < 8; ++k) {
+          const int from = gbase + (LPR * k + e) / 8;  // row LPR k + e is code (e & 7) there
+          const uint32_t w0 = __shfl_sync(gmask, c0, from), w1 = __shfl_sync(gmask, c1, from);
+          dst[LPR * kBlockSize * k] = (uint8_t)((e & 4 ? w1 : w0) >> sh);
         }
+      }
+      continue;
+    }
+    // A[i], B[i]: the elements of pair i, two pairs to a word
+    uint64_t A[2], B[2];
+    auto split = [](const uint4 &v, uint64_t(&x)[2], uint64_t(&z)[2]) {
+      if constexpr (INTER) {
+        x[0] = f32x2(bf16_lo(v.x), bf16_lo(v.y)), z[0] = f32x2(bf16_hi(v.x), bf16_hi(v.y));
+        x[1] = f32x2(bf16_lo(v.z), bf16_lo(v.w)), z[1] = f32x2(bf16_hi(v.z), bf16_hi(v.w));
+      } else {
+        x[0] = bf16x2_to_f32x2(v.x), x[1] = bf16x2_to_f32x2(v.y);
+        z[0] = bf16x2_to_f32x2(v.z), z[1] = bf16x2_to_f32x2(v.w);
+      }
+    };
+    split(raw, A, B);
+    if ((is_q ? a.q_weight : a.k_weight) != nullptr) {
+      const uint64_t sq = fma_f32x2(
+          A[0], A[0], fma_f32x2(A[1], A[1], fma_f32x2(B[0], B[0], mul_f32x2(B[1], B[1]))));
+      float s0, s1;
+      f32x2_split(sq, s0, s1);
+      float ss = s0 + s1;
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(gmask, ss, o);
+      const float inv = rsqrtf(fmaf(ss, 1.0f / D, a.eps));
+      const uint64_t inv2 = f32x2(inv, inv);
+      uint64_t wa[2], wb[2];
+      split(is_q ? qw : kw, wa, wb);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        A[i] = mul_f32x2(mul_f32x2(A[i], inv2), wa[i]);
+        B[i] = mul_f32x2(mul_f32x2(B[i], inv2), wb[i]);
+      }
+    }
+    if (rotates) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint64_t x = A[i];
+        A[i] = fma_f32x2(x, cs[i], mul_f32x2(B[i], ms[i]));
+        B[i] = fma_f32x2(B[i], cs[i], mul_f32x2(x, sn[i]));
+      }
+    }
+    float x[4], z[4];
+    f32x2_split(A[0], x[0], x[1]), f32x2_split(A[1], x[2], x[3]);
+    f32x2_split(B[0], z[0], z[1]), f32x2_split(B[1], z[2], z[3]);
+    if (!F8 || is_q) {
+      uint2 lo, hi;
+      if constexpr (INTER)
+        lo = make_uint2(pack2(x[0], z[0]), pack2(x[1], z[1])),
+        hi = make_uint2(pack2(x[2], z[2]), pack2(x[3], z[3]));
+      else
+        lo = make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3])),
+        hi = make_uint2(pack2(z[0], z[1]), pack2(z[2], z[3]));
+      uint16_t *dst = is_q ? q_out + r * D
+                           : static_cast<uint16_t *>(a.k_cache) +
+                                 (block_row + (r - a.q_heads)) * (kBlockSize * D) + off * D;
+      *reinterpret_cast<uint2 *>(dst + oa) = lo;
+      *reinterpret_cast<uint2 *>(dst + ob) = hi;
+    } else {
+      const int h = r - a.q_heads;
+      const float ks = a.k_scales ? a.k_scales[h] : a.k_scale;
+      if (!(ks > 0.f) || (a.v_scales && !(a.v_scales[h] > 0.f))) {
+        if (e == 0) flag_error(a.err, PKV_DEV_BAD_SCALE);
         continue;
       }
-      float x[8];
-      unpack8(raw[u], x);
-      if ((is_q ? a.q_weight : a.k_weight) != nullptr) {
-        float ss = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-#pragma unroll
-        for (int off = LPR / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(gmask, ss, off);
-        const float inv = rsqrtf(fmaf(ss, 1.0f / D, a.eps));
-        float w[8];
-        unpack8(is_q ? qw : kw, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = x[j] * inv * w[j];
-      }
-      float y[8];
-      if (a.interleaved) {
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          y[j] = x[j] * cs[j] - x[j + 1] * sn[j];
-          y[j + 1] = x[j + 1] * cs[j] + x[j] * sn[j];
-        }
+      const RowDivide div(ks);
+      uint8_t *dst = static_cast<uint8_t *>(a.k_cache) + (block_row + h) * (kBlockSize * D) + off * D;
+      if constexpr (INTER) {
+        *reinterpret_cast<uint32_t *>(dst + oa) = div.codes(x[0], z[0], x[1], z[1]);
+        *reinterpret_cast<uint32_t *>(dst + ob) = div.codes(x[2], z[2], x[3], z[3]);
       } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float o = __shfl_sync(gmask, x[j], partner);
-          y[j] = x[j] * cs[j] + (second ? o : -o) * sn[j];
-        }
-      }
-      if (!rotates) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = x[j];
-      }
-      if (!F8 || is_q) {
-        const uint4 o = make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]),
-                                   pack2(y[6], y[7]));
-        if (is_q)
-          *reinterpret_cast<uint4 *>(a.q_out + t * a.q_out_stride + (int64_t)h * D + e * 8) = o;
-        else
-          reinterpret_cast<uint4 *>(a.k_cache)[row16 * LPR + e] = o;
-      } else {
-        uint32_t c[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          c[j] = __nv_cvt_float2_to_fp8x2(
-              make_float2(__fdiv_rn(y[2 * j], ks), __fdiv_rn(y[2 * j + 1], ks)), __NV_SATFINITE,
-              __NV_E4M3);
-        reinterpret_cast<uint2 *>(a.k_cache)[row16 * LPR + e] =
-            make_uint2((c[0] & 0xffffu) | (c[1] << 16), (c[2] & 0xffffu) | (c[3] << 16));
+        *reinterpret_cast<uint32_t *>(dst + oa) = div.codes(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<uint32_t *>(dst + ob) = div.codes(z[0], z[1], z[2], z[3]);
       }
     }
   }
+}
+
+template <int D, bool F8>
+cudaError_t launch_rope(const RopeArgs &a, dim3 grid, cudaStream_t st) {
+  return a.interleaved
+             ? launch_pdl(qk_norm_rope_write_kernel<D, F8, true>, grid, dim3(kRopeThreads), 0, st, a)
+             : launch_pdl(qk_norm_rope_write_kernel<D, F8, false>, grid, dim3(kRopeThreads), 0, st,
+                          a);
 }
 
 int rope_impl(RopeArgs &a, const uint8_t *pair_axis, int num_axes, int rotary_dim, int num_blocks,
@@ -269,11 +341,9 @@ int rope_impl(RopeArgs &a, const uint8_t *pair_axis, int num_axes, int rotary_di
   const cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e;
   if (head_dim == 128)
-    e = f8 ? launch_pdl(qk_norm_rope_write_kernel<128, true>, grid, dim3(kRopeThreads), 0, st, a)
-           : launch_pdl(qk_norm_rope_write_kernel<128, false>, grid, dim3(kRopeThreads), 0, st, a);
+    e = f8 ? launch_rope<128, true>(a, grid, st) : launch_rope<128, false>(a, grid, st);
   else
-    e = f8 ? launch_pdl(qk_norm_rope_write_kernel<64, true>, grid, dim3(kRopeThreads), 0, st, a)
-           : launch_pdl(qk_norm_rope_write_kernel<64, false>, grid, dim3(kRopeThreads), 0, st, a);
+    e = f8 ? launch_rope<64, true>(a, grid, st) : launch_rope<64, false>(a, grid, st);
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 

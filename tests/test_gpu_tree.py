@@ -174,6 +174,26 @@ def test_write_without_norm_or_rotation_is_the_plain_write(ops, f8):
     assert torch.equal(qo, q) and torch.equal(c[0], c[2]) and torch.equal(c[1], c[3])
 
 
+@pytest.mark.parametrize("scales", [(0.02, 0.015), (1.0, 3.0e-3), (0.5, 448.0), (1e-30, 1e30),
+                                    (3e38, 1e-38), (1.1e-18, 9e17), (0.0078125, 1 / 3)])
+def test_e4m3_codes_of_every_bf16(ops, scales):
+    """Every bf16 pattern as k and as v: the codes of the plain quantising write (a NaN's sign
+    aside), for scales inside and far outside the range of the shared reciprocal."""
+    D, Hkv = 128, 4
+    T = 65536 // (D * Hkv)
+    k = torch.arange(65536, dtype=torch.int32).sub(32768).to(torch.int16).view(T, Hkv, D)
+    k = k.view(torch.bfloat16).cuda()
+    v = k.flip(0).contiguous()
+    slots = torch.arange(T, device="cuda")
+    q = torch.zeros(T, Hkv, D, dtype=torch.bfloat16, device="cuda")
+    c = [torch.zeros(T // BS, Hkv, BS, D, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    ops.paged_qk_norm_rope_write_fp8(q.clone(), q, k, v, None, None, slots, c[0], c[1], *scales)
+    ops.paged_kv_write_fp8(k, v, slots, c[2], c[3], *scales)
+    for a, b in ((c[0], c[2]), (c[1], c[3])):
+        nan = ((a & 0x7F) == 0x7F) & ((b & 0x7F) == 0x7F)
+        assert bool(((a == b) | nan).all()), int((a != b).sum())
+
+
 def test_rope_in_place_far_positions_and_shared_axes(ops):
     """q rotated where it stands in the packed projection, positions up to the largest int32
     (and negative ones), one row of positions for all axes."""
