@@ -478,53 +478,86 @@ def paged_decode_step_fp8(out, q, k_cache, v_cache, block_tables, context_lens, 
 
 
 # ---- drafted trees -------------------------------------------------------------------
-def _call(name, stream, first, others, *args):
-    """Run entry point `name` on the device that holds `first` (and must hold every tensor
-    of `others`), on `stream` or that device's current stream."""
-    dev = first.device
-    for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name}: every tensor must be on {dev}, got one on {t.device}")
+# A step makes these calls once per layer, and for a small batch the Python side of a call
+# would cost more than the kernel: the checks below touch each tensor once (type, device,
+# contiguity) and look for what was wrong only after one has failed.
+_BF16, _U8, _I32, _I64T, _F32, _F64 = (torch.bfloat16, torch.uint8, torch.int32, torch.int64,
+                                       torch.float32, torch.float64)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _fits(index, dtype, tensors):
+    """Whether every tensor is contiguous, of `dtype` and on CUDA device `index`."""
+    for t in tensors:
+        if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+            return False
+    return True
+
+
+def _refuse(call, index, dtype, **tensors):
+    """Raise for the first of the named tensors that _fits() turned down."""
+    for name, t in tensors.items():
+        if not torch.is_tensor(t) or t.dtype is not dtype or not t.is_cuda \
+                or not t.is_contiguous():
+            raise TypeError(f"{call}: {name} must be a contiguous {dtype} CUDA tensor")
+        if t.get_device() != index:
+            raise ValueError(f"{call}: every tensor must be on cuda:{index}, {name} is on "
+                             f"{t.device}")
+
+
+def _index_of(call, name, t):
+    """CUDA device index of the tensor that places a call."""
+    if not t.is_cuda:
+        raise TypeError(f"{call}: {name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _run(call, fn, index, stream, err_flag, *args):
+    """Call fn(*args, err_flag, stream) with device `index` current, on `stream` (a stream
+    object of that device, or a handle) or that device's current stream."""
+    err = None
+    if err_flag is not None:
+        if err_flag.dtype is not _I32 or err_flag.get_device() != index or err_flag.numel() < 1:
+            raise TypeError(f"{call}: err_flag must be an int32 tensor on cuda:{index}")
+        err = err_flag.data_ptr()
     if stream is None:
-        stream = torch.cuda.current_stream(dev).cuda_stream
+        stream = _raw_stream(index)
     elif hasattr(stream, "cuda_stream"):
-        if stream.device != dev:
-            raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on {dev}")
+        if stream.device.index != index:
+            raise ValueError(f"{call}: the stream is on {stream.device}, the tensors on "
+                             f"cuda:{index}")
         stream = stream.cuda_stream
-    if dev.index == torch.cuda.current_device():
-        check(getattr(lib, name)(*args, int(stream)), name)
+    if index == torch.cuda.current_device():
+        code = fn(*args, err, stream)
     else:
-        with torch.cuda.device(dev):
-            check(getattr(lib, name)(*args, int(stream)), name)
+        with torch.cuda.device(index):
+            code = fn(*args, err, stream)
+    if code != 0:
+        raise PagedKVError(code, call)
 
 
-def _i64(name, t):
-    if t.dtype != torch.int64 or not t.is_cuda or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous int64 CUDA tensor")
+def _scale_args(call, index, k_scale, v_scale, num_kv_heads):
+    """(k_scale, v_scale, k_scales pointer, v_scales pointer) of an E4M3 call."""
+    if isinstance(k_scale, torch.Tensor) or isinstance(v_scale, torch.Tensor):
+        if not (isinstance(k_scale, torch.Tensor) and isinstance(v_scale, torch.Tensor)):
+            raise TypeError(f"{call}: k_scale and v_scale must both be numbers or both tensors")
+        if not _fits(index, _F32, (k_scale, v_scale)):
+            _refuse(call, index, _F32, k_scales=k_scale, v_scales=v_scale)
+        if k_scale.shape != (num_kv_heads,) or v_scale.shape != (num_kv_heads,):
+            raise TypeError(f"{call}: k_scales and v_scales must be [num_kv_heads]")
+        return 1.0, 1.0, k_scale.data_ptr(), v_scale.data_ptr()
+    return float(k_scale), float(v_scale), None, None
 
 
-def _err_word(t):
-    if t is not None and (t.dtype != torch.int32 or not t.is_cuda or t.numel() < 1):
-        raise TypeError("err_flag must be an int32 CUDA tensor")
-
-
-def _caches(k_cache, v_cache, f8):
-    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        (_u8_cuda if f8 else _bf16_cuda)(n, t)
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must be [num_blocks][num_kv_heads][16][head_dim]")
-    return k_cache.shape
-
-
-def _scale_args(k_scale, v_scale, num_kv_heads):
-    """(k_scale, v_scale, k_scales pointer, v_scales pointer, tensors) of an E4M3 call."""
-    if torch.is_tensor(k_scale) or torch.is_tensor(v_scale):
-        if not (torch.is_tensor(k_scale) and torch.is_tensor(v_scale)):
-            raise TypeError("k_scale and v_scale must both be numbers or both be tensors")
-        _scales_cuda("k_scales", k_scale, num_kv_heads)
-        _scales_cuda("v_scales", v_scale, num_kv_heads)
-        return 1.0, 1.0, k_scale.data_ptr(), v_scale.data_ptr(), (k_scale, v_scale)
-    return float(k_scale), float(v_scale), None, None, ()
+def _cache_shape(call, index, dtype, k_cache, v_cache):
+    if not _fits(index, dtype, (k_cache, v_cache)):
+        _refuse(call, index, dtype, k_cache=k_cache, v_cache=v_cache)
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError(f"{call}: k_cache and v_cache must be "
+                         "[num_blocks][num_kv_heads][16][head_dim]")
+    return shape
 
 
 def paged_tree_masks(masks, positions, parents, query_start, context_lens, position_base=None,
@@ -533,86 +566,103 @@ def paged_tree_masks(masks, positions, parents, query_start, context_lens, posit
     (int32 [T] or None) of drafted trees from each token's parent (int32 [T], -1 = the cached
     context).  A tree token's position is position_base[s] (default: where the tree starts in
     the context) plus its depth."""
-    _i64("masks", masks)
-    _i32("parents", parents)
-    _i32("query_start", query_start)
-    _i32("context_lens", context_lens)
-    _err_word(err_flag)
-    T, S = parents.shape[0], context_lens.shape[0]
-    if masks.dim() != 2 or masks.shape[0] != T or query_start.shape != (S + 1,):
-        raise ValueError("masks must be [num_tokens][words] and query_start [S+1]")
+    call = "paged_tree_masks"
+    index = _index_of(call, "masks", masks)
+    if not (_fits(index, _I64T, (masks,)) and _fits(index, _I32, (parents, query_start,
+                                                                   context_lens))):
+        _refuse(call, index, _I64T, masks=masks)
+        _refuse(call, index, _I32, parents=parents, query_start=query_start,
+                context_lens=context_lens)
+    T, S = parents.numel(), context_lens.numel()
+    if masks.dim() != 2 or masks.shape[0] != T or query_start.numel() != S + 1:
+        raise ValueError(f"{call}: masks must be [num_tokens][words] and query_start [S+1]")
+    pos = base = None
     if positions is not None:
-        _i32("positions", positions)
-        if positions.shape != (T,):
-            raise ValueError("positions must be [num_tokens]")
+        if not _fits(index, _I32, (positions,)):
+            _refuse(call, index, _I32, positions=positions)
+        if positions.numel() != T:
+            raise ValueError(f"{call}: positions must be [num_tokens]")
+        pos = positions.data_ptr()
     if position_base is not None:
-        _i32("position_base", position_base)
-        if position_base.shape != (S,):
-            raise ValueError("position_base must be [S]")
-    _call("paged_tree_masks", stream, masks,
-          (positions, parents, query_start, context_lens, position_base, err_flag),
-          masks.data_ptr(), _ptr(positions), parents.data_ptr(), query_start.data_ptr(),
-          context_lens.data_ptr(), _ptr(position_base), S, T, masks.shape[1], _ptr(err_flag))
+        if not _fits(index, _I32, (position_base,)):
+            _refuse(call, index, _I32, position_base=position_base)
+        if position_base.numel() != S:
+            raise ValueError(f"{call}: position_base must be [S]")
+        base = position_base.data_ptr()
+    _run(call, lib.paged_tree_masks, index, stream, err_flag, masks.data_ptr(), pos,
+         parents.data_ptr(), query_start.data_ptr(), context_lens.data_ptr(), base, S, T,
+         masks.shape[1])
 
 
-def _head_rows(name, t, T, D):
+def _head_rows(call, name, t, index, T, D):
     """Heads and token stride of a [T][H][D] bf16 tensor whose heads are adjacent."""
-    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 3:
-        raise TypeError(f"{name} must be a bf16 CUDA tensor [num_tokens][heads][head_dim]")
-    H = t.shape[1]
-    if t.shape[0] != T or t.shape[2] != D:
-        raise ValueError(f"{name} must be [num_tokens][heads][head_dim]")
+    if t.dtype is not _BF16 or t.get_device() != index:
+        if t.dtype is not _BF16 or not t.is_cuda:
+            raise TypeError(f"{call}: {name} must be a bf16 CUDA tensor")
+        raise ValueError(f"{call}: every tensor must be on cuda:{index}")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != T or shape[2] != D:
+        raise ValueError(f"{call}: {name} must be [num_tokens][heads][head_dim]")
+    H = shape[1]
     s0, s1, s2 = t.stride()
-    if s2 != 1 or (H > 1 and s1 != D):
-        raise ValueError(f"{name}: heads must be adjacent rows of head_dim elements")
+    if s2 != 1 or (s1 != D and H > 1):
+        raise ValueError(f"{call}: {name}'s heads must be adjacent rows of head_dim elements")
     return H, (s0 if T > 1 else H * D)
 
 
-def _qk_norm_rope_write(name, f8, q_out, q, k, v, positions, inv_freq, slot_mapping, k_cache,
-                        v_cache, scales, q_weight, k_weight, eps, pair_axes, interleaved,
-                        rope_scale, err_flag, stream):
-    NB, Hkv, bs, D = _caches(k_cache, v_cache, f8)
-    _i64("slot_mapping", slot_mapping)
-    _err_word(err_flag)
-    T = slot_mapping.shape[0]
-    Hq, qs = _head_rows("q", q, T, D)
-    Ho, os_ = _head_rows("q_out", q_out, T, D)
-    Hk, ks = _head_rows("k", k, T, D)
-    Hv, vs = _head_rows("v", v, T, D)
+def _qk_norm_rope_write(call, fn, dtype, scales, q_out, q, k, v, positions, inv_freq,
+                        slot_mapping, k_cache, v_cache, q_weight, k_weight, eps, pair_axes,
+                        interleaved, rope_scale, err_flag, stream):
+    index = _index_of(call, "q", q)
+    NB, Hkv, bs, D = _cache_shape(call, index, dtype, k_cache, v_cache)
+    if not _fits(index, _I64T, (slot_mapping,)):
+        _refuse(call, index, _I64T, slot_mapping=slot_mapping)
+    T = slot_mapping.numel()
+    Hq, qs = _head_rows(call, "q", q, index, T, D)
+    Ho, os_ = _head_rows(call, "q_out", q_out, index, T, D)
+    Hk, ks = _head_rows(call, "k", k, index, T, D)
+    Hv, vs = _head_rows(call, "v", v, index, T, D)
     if Ho != Hq or Hk != Hkv or Hv != Hkv:
-        raise ValueError("q_out must have q's heads; k and v the cache's")
-    for n, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _bf16_cuda(n, w)
-            if w.shape != (D,):
-                raise ValueError(f"{n} must be [head_dim]")
-    half = axes = stride = 0
+        raise ValueError(f"{call}: q_out must have q's heads; k and v the cache's")
+    qw = kw = pos = freq = None
+    if q_weight is not None:
+        if not _fits(index, _BF16, (q_weight,)):
+            _refuse(call, index, _BF16, q_weight=q_weight)
+        if q_weight.numel() != D:
+            raise ValueError(f"{call}: q_weight must be [head_dim]")
+        qw = q_weight.data_ptr()
+    if k_weight is not None:
+        if not _fits(index, _BF16, (k_weight,)):
+            _refuse(call, index, _BF16, k_weight=k_weight)
+        if k_weight.numel() != D:
+            raise ValueError(f"{call}: k_weight must be [head_dim]")
+        kw = k_weight.data_ptr()
+    half, axes, stride = 0, 1, 0
     if inv_freq is not None:
+        if not _fits(index, _F64, (inv_freq,)):
+            _refuse(call, index, _F64, inv_freq=inv_freq)
         half = inv_freq.numel()
-        if inv_freq.dtype != torch.float64 or not inv_freq.is_cuda or not inv_freq.is_contiguous():
-            raise TypeError("inv_freq must be a contiguous float64 CUDA tensor")
-        if positions is None or positions.dtype != torch.int32 or not positions.is_cuda:
-            raise TypeError("positions must be an int32 CUDA tensor")
-        if positions.dim() not in (1, 2) or positions.shape[-1] != T or (
-                T > 1 and positions.stride(-1) != 1):
-            raise ValueError("positions must be [num_tokens] or [axes][num_tokens]")
-        axes = positions.shape[0] if positions.dim() == 2 else 1
-        stride = positions.stride(0) if axes > 1 else 0
+        if positions is None or positions.dtype is not _I32 or positions.get_device() != index:
+            raise TypeError(f"{call}: positions must be an int32 tensor on cuda:{index}")
+        shape, strides = positions.shape, positions.stride()
+        if len(shape) not in (1, 2) or shape[-1] != T or (T > 1 and strides[-1] != 1):
+            raise ValueError(f"{call}: positions must be [num_tokens] or [axes][num_tokens]")
+        if len(shape) == 2:
+            axes, stride = shape[0], strides[0]
+        pos, freq = positions.data_ptr(), inv_freq.data_ptr()
     if pair_axes is not None:
         if not isinstance(pair_axes, bytes):
             pair_axes = bytes([int(x) for x in pair_axes])
         if len(pair_axes) != half:
-            raise ValueError("pair_axes must name an axis for each of inv_freq's pairs")
+            raise ValueError(f"{call}: pair_axes must name an axis for each of inv_freq's pairs")
     elif axes > 1:
-        raise ValueError("positions with several axes need pair_axes")
-    tail = () if scales is None else scales[:4]
-    _call(name, stream, q, (q_out, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache,
-                            q_weight, k_weight, err_flag, *(scales[4] if scales else ())),
-          q_out.data_ptr(), os_, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
-          _ptr(q_weight), _ptr(k_weight), eps, _ptr(positions) if half else None, stride,
-          max(axes, 1), pair_axes, _ptr(inv_freq), 2 * half, 1 if interleaved else 0, rope_scale,
-          slot_mapping.data_ptr(), T, k_cache.data_ptr(), v_cache.data_ptr(), NB, Hq, Hkv, D, bs,
-          *tail, _ptr(err_flag))
+        raise ValueError(f"{call}: positions with several axes need pair_axes")
+    if scales is not None:
+        scales = _scale_args(call, index, *scales, Hkv)
+    _run(call, fn, index, stream, err_flag, q_out.data_ptr(), os_, q.data_ptr(), qs, k.data_ptr(),
+         ks, v.data_ptr(), vs, qw, kw, eps, pos, stride, axes, pair_axes, freq, 2 * half,
+         1 if interleaved else 0, rope_scale, slot_mapping.data_ptr(), T, k_cache.data_ptr(),
+         v_cache.data_ptr(), NB, Hq, Hkv, D, bs, *(scales or ()))
 
 
 def paged_qk_norm_rope_write(q_out, q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache,
@@ -623,9 +673,10 @@ def paged_qk_norm_rope_write(q_out, q, k, v, positions, inv_freq, slot_mapping, 
     stride apart (slices of one projection).  inv_freq: float64 [pairs] radians per position
     (None: no rotation); positions: int32 [T] or [axes][T]; pair_axes: the axis of each pair
     (bytes or a sequence of ints) when there are several.  q_out may be q."""
-    _qk_norm_rope_write("paged_qk_norm_rope_write", False, q_out, q, k, v, positions, inv_freq,
-                        slot_mapping, k_cache, v_cache, None, q_weight, k_weight, eps, pair_axes,
-                        interleaved, rope_scale, err_flag, stream)
+    _qk_norm_rope_write("paged_qk_norm_rope_write", lib.paged_qk_norm_rope_write, _BF16, None,
+                        q_out, q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache,
+                        q_weight, k_weight, eps, pair_axes, interleaved, rope_scale, err_flag,
+                        stream)
 
 
 def paged_qk_norm_rope_write_fp8(q_out, q, k, v, positions, inv_freq, slot_mapping, k_cache,
@@ -634,10 +685,10 @@ def paged_qk_norm_rope_write_fp8(q_out, q, k, v, positions, inv_freq, slot_mappi
                                  err_flag=None, stream=None):
     """paged_qk_norm_rope_write into E4M3 caches.  k_scale/v_scale: floats (one scale per
     cache) or float32 CUDA tensors [num_kv_heads] (one scale per KV head)."""
-    scales = _scale_args(k_scale, v_scale, k_cache.shape[1])
-    _qk_norm_rope_write("paged_qk_norm_rope_write_fp8", True, q_out, q, k, v, positions, inv_freq,
-                        slot_mapping, k_cache, v_cache, scales, q_weight, k_weight, eps,
-                        pair_axes, interleaved, rope_scale, err_flag, stream)
+    _qk_norm_rope_write("paged_qk_norm_rope_write_fp8", lib.paged_qk_norm_rope_write_fp8, _U8,
+                        (k_scale, v_scale), q_out, q, k, v, positions, inv_freq, slot_mapping,
+                        k_cache, v_cache, q_weight, k_weight, eps, pair_axes, interleaved,
+                        rope_scale, err_flag, stream)
 
 
 def paged_attention_tree_workspace_size(num_q_heads, num_kv_heads, head_dim,
@@ -658,34 +709,34 @@ def alloc_tree_workspace(num_q_heads, num_kv_heads, head_dim, max_query_len, dev
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _attention_tree(name, f8, out, q, k_cache, v_cache, block_tables, context_lens, query_start,
-                    tree_masks, scale, scales, max_query_len, workspace, err_flag, stream):
-    NB, Hkv, bs, D = _caches(k_cache, v_cache, f8)
-    _bf16_cuda("out", out)
-    _bf16_cuda("q", q)
-    _i32("block_tables", block_tables)
-    _i32("context_lens", context_lens)
-    _i32("query_start", query_start)
-    _i64("tree_masks", tree_masks)
-    _err_word(err_flag)
-    S = context_lens.shape[0]
-    if q.dim() != 3 or q.shape[2] != D or out.shape != q.shape:
-        raise ValueError("q and out must be [num_tokens][num_q_heads][head_dim]")
-    T, Hq, _ = q.shape
-    if block_tables.dim() != 2 or block_tables.shape[0] != S or query_start.shape != (S + 1,):
-        raise ValueError("block_tables must be [S][max_blocks] and query_start [S+1]")
-    if tree_masks.dim() != 2 or tree_masks.shape[0] != T:
-        raise ValueError("tree_masks must be [num_tokens][words]")
-    if not workspace.is_cuda or not workspace.is_contiguous():
-        raise TypeError("workspace must be a contiguous CUDA tensor")
-    kv_scales = () if scales is None else scales[:4]
-    _call(name, stream, q, (out, k_cache, v_cache, block_tables, context_lens, query_start,
-                            tree_masks, workspace, err_flag, *(scales[4] if scales else ())),
-          out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-          block_tables.data_ptr(), context_lens.data_ptr(), query_start.data_ptr(),
-          tree_masks.data_ptr(), tree_masks.shape[1], S, T, block_tables.shape[1], Hq, Hkv, D, bs,
-          NB, scale, *kv_scales, max_query_len, workspace.data_ptr(),
-          workspace.numel() * workspace.element_size(), _ptr(err_flag))
+def _attention_tree(call, fn, dtype, scales, out, q, k_cache, v_cache, block_tables, context_lens,
+                    query_start, tree_masks, scale, max_query_len, workspace, err_flag, stream):
+    index = _index_of(call, "q", q)
+    NB, Hkv, bs, D = _cache_shape(call, index, dtype, k_cache, v_cache)
+    if not (_fits(index, _BF16, (out, q)) and _fits(index, _I32, (
+            block_tables, context_lens, query_start)) and _fits(index, _I64T, (tree_masks,))
+            and _fits(index, workspace.dtype, (workspace,))):
+        _refuse(call, index, _BF16, out=out, q=q)
+        _refuse(call, index, _I32, block_tables=block_tables, context_lens=context_lens,
+                query_start=query_start)
+        _refuse(call, index, _I64T, tree_masks=tree_masks)
+        _refuse(call, index, workspace.dtype, workspace=workspace)
+    S = context_lens.numel()
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != D or out.shape != shape:
+        raise ValueError(f"{call}: q and out must be [num_tokens][num_q_heads][head_dim]")
+    T, Hq, _ = shape
+    bt, tm = block_tables.shape, tree_masks.shape
+    if len(bt) != 2 or bt[0] != S or query_start.numel() != S + 1:
+        raise ValueError(f"{call}: block_tables must be [S][max_blocks] and query_start [S+1]")
+    if len(tm) != 2 or tm[0] != T:
+        raise ValueError(f"{call}: tree_masks must be [num_tokens][words]")
+    if scales is not None:
+        scales = _scale_args(call, index, *scales, Hkv)
+    _run(call, fn, index, stream, err_flag, out.data_ptr(), q.data_ptr(), k_cache.data_ptr(),
+         v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+         query_start.data_ptr(), tree_masks.data_ptr(), tm[1], S, T, bt[1], Hq, Hkv, D, bs, NB,
+         scale, *(scales or ()), max_query_len, workspace.data_ptr(), workspace.nbytes)
 
 
 def paged_attention_tree(out, q, k_cache, v_cache, block_tables, context_lens, query_start,
@@ -693,9 +744,9 @@ def paged_attention_tree(out, q, k_cache, v_cache, block_tables, context_lens, q
     """Attention of drafted trees: rows query_start[s] .. query_start[s+1]-1 of q [T][Hq][D]
     are the last tokens of sequence s; each sees the cached tokens before the tree and the tree
     tokens its tree_masks row (int64 [T][W]) names.  workspace: alloc_tree_workspace."""
-    _attention_tree("paged_attention_tree", False, out, q, k_cache, v_cache, block_tables,
-                    context_lens, query_start, tree_masks, scale, None, max_query_len, workspace,
-                    err_flag, stream)
+    _attention_tree("paged_attention_tree", lib.paged_attention_tree, _BF16, None, out, q, k_cache,
+                    v_cache, block_tables, context_lens, query_start, tree_masks, scale,
+                    max_query_len, workspace, err_flag, stream)
 
 
 def paged_attention_tree_fp8(out, q, k_cache, v_cache, block_tables, context_lens, query_start,
@@ -703,44 +754,45 @@ def paged_attention_tree_fp8(out, q, k_cache, v_cache, block_tables, context_len
                              err_flag=None, stream=None):
     """paged_attention_tree over E4M3 caches.  k_scale/v_scale: floats (one scale per cache)
     or float32 CUDA tensors [num_kv_heads] (one scale per KV head)."""
-    scales = _scale_args(k_scale, v_scale, k_cache.shape[1])
-    _attention_tree("paged_attention_tree_fp8", True, out, q, k_cache, v_cache, block_tables,
-                    context_lens, query_start, tree_masks, scale, scales, max_query_len,
-                    workspace, err_flag, stream)
+    _attention_tree("paged_attention_tree_fp8", lib.paged_attention_tree_fp8, _U8,
+                    (k_scale, v_scale), out, q, k_cache, v_cache, block_tables, context_lens,
+                    query_start, tree_masks, scale, max_query_len, workspace, err_flag, stream)
 
 
-def _tree_commit(name, f8, k_cache, v_cache, slot_mapping, query_start, accepted, accepted_lens,
-                 dst_slots, err_flag, stream):
-    NB, Hkv, bs, D = _caches(k_cache, v_cache, f8)
-    _i64("slot_mapping", slot_mapping)
-    _i32("query_start", query_start)
-    _i32("accepted", accepted)
-    _i32("accepted_lens", accepted_lens)
-    _err_word(err_flag)
-    S = accepted_lens.shape[0]
-    if accepted.dim() != 2 or accepted.shape[0] != S or query_start.shape != (S + 1,):
-        raise ValueError("accepted must be [S][max_accept] and query_start [S+1]")
+def _tree_commit(call, fn, dtype, k_cache, v_cache, slot_mapping, query_start, accepted,
+                 accepted_lens, dst_slots, err_flag, stream):
+    index = _index_of(call, "k_cache", k_cache)
+    NB, Hkv, bs, D = _cache_shape(call, index, dtype, k_cache, v_cache)
+    if not (_fits(index, _I64T, (slot_mapping,)) and
+            _fits(index, _I32, (query_start, accepted, accepted_lens))):
+        _refuse(call, index, _I64T, slot_mapping=slot_mapping)
+        _refuse(call, index, _I32, query_start=query_start, accepted=accepted,
+                accepted_lens=accepted_lens)
+    S, shape = accepted_lens.numel(), accepted.shape
+    if len(shape) != 2 or shape[0] != S or query_start.numel() != S + 1:
+        raise ValueError(f"{call}: accepted must be [S][max_accept] and query_start [S+1]")
+    dst = None
     if dst_slots is not None:
-        _i64("dst_slots", dst_slots)
-        if dst_slots.shape != accepted.shape:
-            raise ValueError("dst_slots must have accepted's shape")
-    _call(name, stream, k_cache, (v_cache, slot_mapping, query_start, accepted, accepted_lens,
-                                  dst_slots, err_flag),
-          k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), query_start.data_ptr(),
-          accepted.data_ptr(), accepted_lens.data_ptr(), _ptr(dst_slots), S,
-          slot_mapping.shape[0], accepted.shape[1], NB, Hkv, D, bs, _ptr(err_flag))
+        if not _fits(index, _I64T, (dst_slots,)):
+            _refuse(call, index, _I64T, dst_slots=dst_slots)
+        if dst_slots.shape != shape:
+            raise ValueError(f"{call}: dst_slots must have accepted's shape")
+        dst = dst_slots.data_ptr()
+    _run(call, fn, index, stream, err_flag, k_cache.data_ptr(), v_cache.data_ptr(),
+         slot_mapping.data_ptr(), query_start.data_ptr(), accepted.data_ptr(),
+         accepted_lens.data_ptr(), dst, S, slot_mapping.numel(), shape[1], NB, Hkv, D, bs)
 
 
 def paged_tree_commit(k_cache, v_cache, slot_mapping, query_start, accepted, accepted_lens,
                       dst_slots=None, err_flag=None, stream=None):
     """Move the K/V rows of each sequence's accepted tree tokens (accepted int32 [S][A], the
     first accepted_lens[s] of row s) to the tree's first slots, or to dst_slots [S][A]."""
-    _tree_commit("paged_tree_commit", False, k_cache, v_cache, slot_mapping, query_start, accepted,
-                 accepted_lens, dst_slots, err_flag, stream)
+    _tree_commit("paged_tree_commit", lib.paged_tree_commit, _BF16, k_cache, v_cache, slot_mapping,
+                 query_start, accepted, accepted_lens, dst_slots, err_flag, stream)
 
 
 def paged_tree_commit_fp8(k_cache, v_cache, slot_mapping, query_start, accepted, accepted_lens,
                           dst_slots=None, err_flag=None, stream=None):
     """paged_tree_commit over E4M3 caches."""
-    _tree_commit("paged_tree_commit_fp8", True, k_cache, v_cache, slot_mapping, query_start,
-                 accepted, accepted_lens, dst_slots, err_flag, stream)
+    _tree_commit("paged_tree_commit_fp8", lib.paged_tree_commit_fp8, _U8, k_cache, v_cache,
+                 slot_mapping, query_start, accepted, accepted_lens, dst_slots, err_flag, stream)
