@@ -63,7 +63,6 @@ constexpr int kLaunchRegs = 80, kSoftmaxRegs = 128, kOtherRegs = 56;
 static_assert(128 * kSoftmaxRegs + 256 * kOtherRegs <= 384 * kLaunchRegs, "register split");
 constexpr uint32_t kTmemColumns = 256;
 constexpr int kMaxRowTiles = 64;  // row tiles of one launch
-constexpr int kMinRun = 1;        // least key tiles per CTA
 
 struct TreeArgs {
   uint16_t *out;                // [T][Hq][D] bf16
@@ -80,11 +79,16 @@ struct TreeArgs {
   const float *k_scales, *v_scales;  // [Hkv] or null
   int runs;                     // CTAs that share the key tiles
   int m0, row_tiles;            // this launch's row tiles m0 .. m0 + row_tiles - 1
-  int4 *join;                   // [CTAs] {s, KV head, row tile, parts}: what starts and does
-                                // not end in a CTA
+  struct TreeJoin *join;        // [CTAs] what starts and does not end in a CTA
   float *part_lse;              // [CTAs][2][128] log2-sum-exp2
-  float *part_o;                // [CTAs][2][128][D] normalised
+  float4 *part_o;               // [CTAs][2][D / 4][128 rows] normalised: a warp's rows store
+                                // and load side by side
   int32_t *err;
+};
+
+struct __align__(16) TreeJoin {
+  int q0, rows, g, m;  // first token, rows of the sequence, KV head, row tile
+  int parts, pad[3];   // 0: nothing to join
 };
 
 struct SeqInfo {
@@ -111,7 +115,8 @@ __device__ __forceinline__ SeqInfo seq_info(const TreeArgs &a, int s, bool flag)
 
 // A CTA's run of key tiles, filled by plan_run.
 struct Plan {
-  unsigned long long tiles[kMaxRowTiles];  // key tiles of row tile m (all KV heads)
+  unsigned long long tiles[kMaxRowTiles];  // key tiles of row tile m (all KV heads); later the
+                                           // ring of segments
   unsigned long long warp_sum[tree_threads(true) / 32];
   unsigned long long off;  // first tile within sequence s (KV heads end to end)
   long long left;          // tiles of the run
@@ -120,52 +125,71 @@ struct Plan {
   int s, m;
 };
 
-// Which key tiles this CTA runs (all threads; the result in *p after the last barrier).
+// floor(a b / c), b <= c, without a 128-bit product: b and c lose low bits they do not need.
+__device__ __forceinline__ int share(int a, unsigned long long b, unsigned long long c) {
+  while (c >> 48) b >>= 1, c >>= 1;
+  return (int)((unsigned long long)a * b / c);
+}
+
+// Which key tiles this CTA runs (all threads; the result in *p after the last barrier).  Short
+// on purpose: code that runs once is bound by the instruction fetch, ~20 cycles each.
 template <int kThreads>
 __device__ __forceinline__ void plan_run(const TreeArgs &a, Plan *p) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid < kMaxRowTiles) p->tiles[tid] = 0;
+  const bool one = a.row_tiles == 1;
+  if (!one && tid < kMaxRowTiles) p->tiles[tid] = 0;
   if (tid == 0) p->left = 0;
-  __syncthreads();
-  unsigned long long mine = 0;  // of the last row tile of each sequence, one row tile only
+  if (!one) __syncthreads();
+  unsigned long long mine = 0;
+#pragma unroll 1
   for (int s = tid; s < a.num_seqs; s += kThreads) {
     const SeqInfo i = seq_info(a, s, blockIdx.x == 0);
     const int last = min(i.row_tiles - a.m0, a.row_tiles);
     if (i.tiles == 0 || last <= 0) continue;
-    if (a.row_tiles == 1)
-      mine += i.tiles;
-    else
-      atomicAdd(&p->tiles[last - 1], (unsigned long long)i.tiles);
+    mine += i.tiles;
+    if (!one) atomicAdd(&p->tiles[last - 1], (unsigned long long)i.tiles);
   }
-  if (a.row_tiles == 1) {
-#pragma unroll
+  if (one) {
+#pragma unroll 1
     for (int off = 16; off > 0; off >>= 1) mine += __shfl_xor_sync(kFullMask, mine, off);
-    if (lane == 0 && mine) atomicAdd(&p->tiles[0], mine);
+    if (lane == 0) p->warp_sum[warp] = mine;
   }
   __syncthreads();
   if (tid == 0) {
     unsigned long long sum = 0, total = 0;
-    for (int m = a.row_tiles - 1; m >= 0; --m) {
-      sum += p->tiles[m] * (unsigned)a.kv_heads;
-      p->tiles[m] = sum;
-      total += sum;
+    if (one) {
+#pragma unroll 1
+      for (int w = 0; w < kThreads / 32; ++w) sum += p->warp_sum[w];
+      p->tiles[0] = total = sum * (unsigned)a.kv_heads;
+    } else {
+#pragma unroll 1
+      for (int m = a.row_tiles - 1; m >= 0; --m) {
+        sum += p->tiles[m] * (unsigned)a.kv_heads;
+        p->tiles[m] = sum;
+        total += sum;
+      }
     }
     int at = 0;
+#pragma unroll 1
     for (int m = 0; m < a.row_tiles && p->tiles[m]; ++m) {
       const unsigned long long w = p->tiles[m];
-      int n = total == w ? a.runs : (int)((double)a.runs * (double)w / (double)total);
-      const unsigned long long most = (w + kMinRun - 1) / kMinRun;
-      if ((unsigned long long)n > most) n = (int)most;
+      int n = one ? a.runs : share(a.runs, w, total);
+      if ((unsigned long long)n > w) n = (int)w;
       if (n < 1) n = 1;
-      if ((int)blockIdx.x < at + n) {
-        const int c = (int)blockIdx.x - at;
+      const int c = (int)blockIdx.x - at;
+      if (c < n) {
+        unsigned long long q, r;
+        if (w >> 32)
+          q = w / (unsigned)n, r = w % (unsigned)n;
+        else
+          q = (unsigned)w / (unsigned)n, r = (unsigned)w % (unsigned)n;
         p->m = a.m0 + m;
         p->ctas = n;
         p->cta = c;
-        p->cta_tiles = (long long)(w / n);
-        p->extra = (long long)(w % n);
-        p->left = p->cta_tiles + (c < p->extra ? 1 : 0);
-        p->off = (unsigned long long)c * p->cta_tiles + min((long long)c, p->extra);
+        p->cta_tiles = (long long)q;
+        p->extra = (long long)r;
+        p->left = (long long)q + (c < (long long)r ? 1 : 0);
+        p->off = (unsigned)c * q + min((long long)c, (long long)r);
         break;
       }
       at += n;
@@ -176,8 +200,8 @@ __device__ __forceinline__ void plan_run(const TreeArgs &a, Plan *p) {
   const unsigned long long u0 = p->off;
   const int m = p->m;
   unsigned long long base = 0;
+#pragma unroll 1
   for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) {
-    __syncthreads();
     const int s = s0 + tid;
     unsigned long long n = 0;
     if (s < a.num_seqs) {
@@ -185,33 +209,40 @@ __device__ __forceinline__ void plan_run(const TreeArgs &a, Plan *p) {
       if (i.row_tiles > m) n = (unsigned long long)i.tiles * a.kv_heads;
     }
     unsigned long long incl = n;
-#pragma unroll
+#pragma unroll 1
     for (int off = 1; off < 32; off <<= 1) {
       const unsigned long long v = __shfl_up_sync(kFullMask, incl, off);
       if (lane >= off) incl += v;
     }
     if (lane == 31) p->warp_sum[warp] = incl;
     __syncthreads();
-    unsigned long long before = base, all = base;
+    unsigned long long first = base + incl - n;
+#pragma unroll 1
     for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += p->warp_sum[w];
-      all += p->warp_sum[w];
+      const unsigned long long v = p->warp_sum[w];
+      if (w < warp) first += v;
+      base += v;
     }
-    const unsigned long long first = before + incl - n;
     if (n && u0 >= first && u0 < first + n) {
       p->s = s;
       p->off = u0 - first;
     }
-    base = all;
-    if (u0 < all) break;
+    if (u0 < base) break;
+    __syncthreads();
   }
   __syncthreads();
 }
 
-// The segments of a run in order; every warp walks them for itself.
-struct Segment {
+// The segments of a run.  The K warp walks them in order, ahead of everyone, and hands them on
+// through a small ring in shared memory; one with no tiles ends the run.  It is at most eight
+// segments ahead of the slowest reader: K of tile t is copied once S of tile t - KS is done,
+// which the softmax warps' work on tile t - KS - 1 precedes, and the ring is written one tile
+// before that copy.
+struct __align__(16) Segment {
   int s, g, q0, L, ctx, tiles, j0, j1;
 };
+constexpr int kSegRing = 8;
+static_assert(kSegRing * sizeof(Segment) <= kMaxRowTiles * sizeof(unsigned long long), "ring");
 
 struct Walk {
   const TreeArgs &a;
@@ -256,19 +287,21 @@ struct TreeLayout {
   static constexpr int VS = F8 && D == 128 ? 2 : 3;       // V ring (f16 values of an E4M3 cache)
   static constexpr int kVSlot = kHalves * kHalf;
   static constexpr int RS = F8 ? 4 : 0;                   // V codes on their way to the V ring
-  // What of Q is not in TMEM: bf16 its columns 64..127, E4M3 (D 128) its second term.
+  // What of Q is not in TMEM (bf16 its columns 64..127, E4M3 at D 128 its second term), and
+  // the finished rows on their way out.
   static constexpr int kQ = 0;
-  static constexpr int kK = (kHalves - 1) * kTileRows * 128;
+  static constexpr int kK = kTileRows * 128;
   static constexpr int kV = kK + KS * kKSlot;
   static constexpr int kRawV = kV + VS * kVSlot;
   static constexpr int kBars = kRawV + RS * kRaw;
-  static constexpr int kNumBars = 2 * KS + 2 * VS + 7 + 2 * RS;
+  static constexpr int kNumBars = 2 * KS + 2 * VS + 7 + 2 * RS + kSegRing;
   static constexpr int kMisc = kBars + kNumBars * 8;  // TMEM address, abort flag, V marks
-  static constexpr int kPlan = kMisc + 96;
+  static constexpr int kPlan = (kMisc + 80 + 15) / 16 * 16;  // holds the segments: 16-byte loads
   static constexpr int kSmem = kPlan + (int)sizeof(Plan);
   // at least 78 KB, so that no more than two CTAs share an SM (256 TMEM columns each)
   static constexpr int kSmemLaunch = kSmem > 78 * 1024 ? kSmem : 78 * 1024;
   static_assert(2 * (kSmemLaunch + 1024) <= 228 * 1024, "two CTAs per SM");
+  static_assert(kPlan % alignof(Segment) == 0 && kBars % 8 == 0, "alignment");
 };
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -315,7 +348,7 @@ __device__ __forceinline__ uint64_t visible_bits(const uint64_t *mask, int t0, i
 }
 
 // The values that were taken out of a row's products because they are not finite, added to
-// the row's stored result (bf16 or fp32) where the row sees them.
+// the row's stored result (a bf16 row, or a part's) where the row sees them.
 template <int D, bool F8>
 __device__ __noinline__ void add_odd_values(const TreeArgs &a, const Segment &seg,
                                             const uint64_t *mask, uint32_t tiles, uint16_t *out,
@@ -341,7 +374,7 @@ __device__ __noinline__ void add_odd_values(const TreeArgs &a, const Segment &se
         if (out)
           out[d] = f32_to_bf16(bf16_to_f32(out[d]) + v);
         else
-          part[d] += v;
+          part[(d >> 2) * (4 * kTileRows) + (d & 3)] += v;
       }
     }
   }
@@ -365,13 +398,14 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
   const uint32_t s_full = v_empty + 8 * VS, s_free = s_full + 8, p_full = s_free + 8;
   const uint32_t o_done = p_full + 8, fin_s = o_done + 8, fin_o = fin_s + 8;
   const uint32_t q_full = fin_o + 8, raw_full = q_full + 8, raw_empty = raw_full + 8 * RS;
+  const uint32_t seg_full = raw_empty + 8 * RS;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Lay::kMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   // Marks of V tiles that held a value not finite.  E4M3: [ring slot], 1 + the number of the
   // CTA's tile that had one.  bf16: [tile of the tree], the number of the segment that did.
   volatile int *v_bad = abort_flag + 1;
   constexpr int kMarks = F8 ? VS : PKV_TREE_MAX_TOKENS / kTileKeys + 1;
-  static_assert(8 + 4 * kMarks <= 96, "marks");
+  static_assert(8 + 4 * kMarks <= 80, "marks");
   Plan *plan = reinterpret_cast<Plan *>(smem + Lay::kPlan);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -391,6 +425,7 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
     mbar_init(fin_s, 1);
     mbar_init(fin_o, 1);
     mbar_init(q_full, 4);
+    for (int i = 0; i < kSegRing; ++i) mbar_init(seg_full + 8 * i, 1);
     for (int i = 0; i < RS; ++i) {
       mbar_init(raw_full + 8 * i, kTileBlocks);
       mbar_init(raw_empty + 8 * i, 4);
@@ -403,7 +438,7 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
   pdl_wait();
   plan_run<tree_threads(F8)>(a, plan);
   if (plan->left == 0) {
-    if (threadIdx.x == 0) a.join[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (threadIdx.x == 0) a.join[blockIdx.x].parts = 0;
     return;
   }
   if (warp == 4) alloc(smem_u32(tmem_slot), kTmemColumns);
@@ -413,8 +448,15 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
   const uint32_t tmem = *tmem_slot;
   const uint32_t tS = tmem, tP = tmem + 64, tQ = tmem + 96, tO = tmem + 128;
   const int G = a.group, r0 = plan->m * kTileRows;
-  Walk walk(a, *plan);
+  Segment *ring_seg = reinterpret_cast<Segment *>(plan->tiles);
   Segment seg;
+  // The run's segment n; false: the run is over (or a wait gave up).
+  auto segment = [&](int n) {
+    if (!mbar_wait(seg_full + 8 * (n % kSegRing), (uint32_t)(n / kSegRing) & 1u, abort_flag, a.err))
+      return false;
+    seg = ring_seg[n % kSegRing];
+    return seg.j1 > seg.j0;
+  };
 
   if (warp < 4) {
     if constexpr (F8) set_regs_up<kSoftmaxRegs>();
@@ -425,8 +467,8 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
     int jt = 0;   // tiles done (the barriers' phases)
     int nseg = 0; // segments begun
     bool ok = true;
-    if (t == 0) a.join[blockIdx.x] = make_int4(0, 0, 0, 0);
-    while (ok && walk.next(seg)) {
+    if (t == 0) a.join[blockIdx.x].parts = 0;
+    while (ok && segment(nseg)) {
       ++nseg;
       const int rows = seg.L * G;
       const bool valid = r < rows, live = r0 + warp * 32 < rows;
@@ -444,17 +486,13 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
       const uint4 *qrow = reinterpret_cast<const uint4 *>(a.q + row);
       if constexpr (!F8) {
         // columns 0..63 to TMEM (two 16-bit elements per column), 64..127 to shared memory
-#pragma unroll 1
-        for (int half = 0; half < H; ++half) {
-          uint4 v[8];
+        uint4 v[8 * H];
 #pragma unroll
-          for (int c = 0; c < 8; ++c) v[c] = valid ? qrow[8 * half + c] : make_uint4(0u, 0u, 0u, 0u);
-          if (half == 0)
-            tmem_st32(tQ + lane_base, reinterpret_cast<uint32_t (&)[32]>(v));
-          else
+        for (int c = 0; c < 8 * H; ++c) v[c] = valid ? qrow[c] : make_uint4(0u, 0u, 0u, 0u);
+        tmem_st32(tQ + lane_base, reinterpret_cast<uint32_t (&)[32]>(v));
 #pragma unroll
-            for (int c = 0; c < 8; ++c) st_shared_v4(sQ + t * 128 + ((c ^ (t & 7)) << 4), v[c]);
-        }
+        for (int c = 8; c < 8 * H; ++c)
+          st_shared_v4(sQ + t * 128 + (((c & 7) ^ (t & 7)) << 4), v[c]);
       } else {
         // The score product is one of E4M3 with E4M3, so that K's codes enter it as they lie
         // in the cache.  q is the sum of two E4M3 terms, q 2^e = q1 + q2, e putting the row's
@@ -660,40 +698,61 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
       const bool whole = seg.j0 == 0 && seg.j1 == seg.tiles;
       const float inv = l == 0.f ? 0.f : vs / l;
       const size_t part = ((size_t)blockIdx.x * 2 + (seg.j0 > 0 ? 0 : 1)) * kTileRows + t;
-      if (!whole && valid) a.part_lse[part] = l == 0.f ? -INFINITY : m + log2f(l);
+      if (whole) {
+        // through this warp's rows of the staging region, so that a row's 128 bytes leave by
+        // adjacent lanes
+        const uint32_t stage = sQ + t * 128;
 #pragma unroll 1
-      for (int cc = 0; cc < D / 32; ++cc) {
-        uint32_t o[32];
-        tmem_ld32(tO + 32 * cc + lane_base, o);
-        wait_ld();
+        for (int half = 0; half < H; ++half) {
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t o[8];
+            tmem_ld8(tO + 64 * half + 8 * c + lane_base, o);
+            wait_ld();
+            uint32_t w[4];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
-        if (!valid) continue;
-        if (whole) {
-          uint4 *dst = reinterpret_cast<uint4 *>(a.out + row + 32 * cc);
+            for (int e = 0; e < 4; ++e)
+              w[e] = pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+            st_shared_v4(stage + ((c ^ (t & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+          }
+          __syncwarp();
+#pragma unroll 1
+          for (int it = 0; it < 8; ++it) {
+            const int rr = warp * 32 + it * 4 + (lane >> 3), c = lane & 7, ro = r0 + rr;
+            if (ro < rows)
+              *reinterpret_cast<uint4 *>(
+                  a.out + ((size_t)(seg.q0 + ro / G) * a.q_heads + seg.g * G + ro % G) * D +
+                  64 * half + 8 * c) = ld_shared_v4(sQ + rr * 128 + ((c ^ (rr & 7)) << 4));
+          }
+          __syncwarp();
+        }
+      } else {
+        if (valid) a.part_lse[part] = l == 0.f ? -INFINITY : m + log2f(l);
+        float4 *dst = a.part_o + (part - t) * (D / 4) + t;
+#pragma unroll 1
+        for (int c = 0; c < D / 8; ++c) {
+          uint32_t o[8];
+          tmem_ld8(tO + 8 * c + lane_base, o);
+          wait_ld();
+          if (valid)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            dst[e] = make_uint4(
-                pack_bf16(__uint_as_float(o[8 * e]), __uint_as_float(o[8 * e + 1])),
-                pack_bf16(__uint_as_float(o[8 * e + 2]), __uint_as_float(o[8 * e + 3])),
-                pack_bf16(__uint_as_float(o[8 * e + 4]), __uint_as_float(o[8 * e + 5])),
-                pack_bf16(__uint_as_float(o[8 * e + 6]), __uint_as_float(o[8 * e + 7])));
-        } else {
-          uint4 *dst = reinterpret_cast<uint4 *>(a.part_o + part * D + 32 * cc);
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < 2; ++e)
+              dst[(2 * c + e) * kTileRows] =
+                  make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                              __uint_as_float(o[4 * e + 2]) * inv,
+                              __uint_as_float(o[4 * e + 3]) * inv);
         }
       }
       if (__builtin_expect(bad != 0 && valid, 0))
-        add_odd_values<D, F8>(a, seg, mask, bad, whole ? a.out + row : nullptr,
-                              whole ? nullptr : a.part_o + part * D);
+        add_odd_values<D, F8>(
+            a, seg, mask, bad, whole ? a.out + row : nullptr,
+            whole ? nullptr : reinterpret_cast<float *>(a.part_o + (part - t) * (D / 4) + t));
       if (t == 0 && seg.j0 == 0 && !whole) {
         // the CTAs that run the rest of this pair's key tiles
         int parts = 1;
         for (long long rest = seg.tiles - seg.j1; rest > 0; ++parts)
           rest -= plan->cta_tiles + (plan->cta + parts < plan->extra ? 1 : 0);
-        a.join[blockIdx.x] = make_int4(seg.s, seg.g, plan->m, parts);
+        a.join[blockIdx.x] = TreeJoin{seg.q0, rows, seg.g, plan->m, parts, {0, 0, 0}};
       }
     }
     fence_before();
@@ -703,7 +762,7 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
     // ---------------- S warp: lane 0 issues S = Q K^T ----------------
     constexpr uint32_t id = F8 ? idesc_e4m3(kTileRows, kTileKeys) : idesc(kTileRows, kTileKeys, false, false);
     int jt = 0, ok = 1;
-    for (int nseg = 0; ok && walk.next(seg); ++nseg) {
+    for (int nseg = 0; ok && segment(nseg); ++nseg) {
       if (lane == 0) ok = mbar_spin_wait(q_full, (uint32_t)nseg & 1u, abort_flag, a.err);
       ok = __shfl_sync(kFullMask, ok, 0);  // Q is staged
       if (!ok) break;
@@ -756,7 +815,7 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
     // bf16: V [keys][D] (MN-major); E4M3: V widened to [D][keys] (K-major)
     constexpr uint32_t id = idesc(kTileRows, D, F8, !F8);
     int jt = 0, ok = 1;
-    while (ok && walk.next(seg)) {
+    for (int nseg = 0; ok && segment(nseg); ++nseg) {
       for (int j = seg.j0; j < seg.j1; ++j, ++jt) {
         const int sb = jt % VS;
         if (lane == 0)
@@ -798,10 +857,30 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
     const uint32_t full = F8 && is_v ? raw_full : is_v ? v_full : k_full;
     const uint32_t empty = F8 && is_v ? raw_empty : is_v ? v_empty : k_empty;
     const uint32_t ring = F8 && is_v ? base + Lay::kRawV : is_v ? sV : sK;
-    Walk ahead(walk);
-    Segment as;
-    bool more = ahead.next(as);
-    int aj = as.j0, issued = 0, slot_in = 0;
+    Walk walk(a, *plan);  // K warp
+    int nseg = 0;
+    // The next segment: the K warp finds and publishes it and asks for its Q rows, the V warp
+    // takes it from the ring.
+    auto advance = [&]() {
+      if (is_v) return segment(nseg++);
+      if (!walk.next(seg)) seg.j0 = seg.j1 = 0;
+      if (lane == 0) {
+        ring_seg[nseg % kSegRing] = seg;
+        mbar_arrive(seg_full + 8 * (nseg % kSegRing));
+      }
+      ++nseg;
+      if (seg.j0 == seg.j1) return false;
+#pragma unroll 1
+      for (int r = r0 + lane; r < min(r0 + kTileRows, seg.L * G); r += 32) {
+        const uint16_t *p = a.q + ((size_t)(seg.q0 + r / G) * a.q_heads + seg.g * G + r % G) * D;
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(p + 64 * h));
+      }
+      return true;
+    };
+    bool more = advance();
+    int aj = seg.j0, issued = 0, slot_in = 0;
     uint32_t empty_parity = 1;  // of the ring's previous round
     // The table's entry of key tile j for this lane's block (INT_MIN: past the context).  Read
     // one tile before it is looked at, so that nothing waits for the load.
@@ -810,20 +889,20 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
       if (lane >= kTileBlocks || tok >= g.ctx) return INT_MIN;
       return a.block_tables[(size_t)g.s * a.max_blocks + tok / kBlockSize];
     };
-    int next_blk = more ? block_of(as, aj) : INT_MIN;
+    int next_blk = more ? block_of(seg, aj) : INT_MIN;
     // Queues the run's next tile once its slot is free; false: gave up.
     auto issue = [&]() {
       int blk = next_blk;
-      const int g = as.g;
+      const int g = seg.g;
       if (blk != INT_MIN && (unsigned)blk >= (unsigned)a.num_blocks) {
         flag_error(a.err, PKV_DEV_BAD_BLOCK);
         blk = INT_MIN;
       }
-      if (++aj >= as.j1) {
-        more = ahead.next(as);
-        aj = as.j0;
+      if (++aj >= seg.j1) {
+        more = advance();
+        aj = seg.j0;
       }
-      if (more) next_blk = block_of(as, aj);  // one tile ahead
+      if (more) next_blk = block_of(seg, aj);  // one tile ahead
       if (issued >= slots && !mbar_wait(empty + 8 * slot_in, empty_parity, abort_flag, a.err))
         return false;
       if (lane < kTileBlocks) {
@@ -850,10 +929,8 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
       if (++slot_in == slots) slot_in = 0, empty_parity ^= 1;
       return true;
     };
-    if (lane < kTileBlocks)
-      while (more && issue()) {
-      }
-    __syncwarp();
+    while (more && __all_sync(kFullMask, issue())) {
+    }
     if (lane == 0 && *abort_flag)
       for (int j = max(0, issued - slots); j < issued; ++j)
         mbar_drain(full + 8 * (j % slots), (uint32_t)(j / slots) & 1u);
@@ -864,7 +941,7 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
     {
       bool ok = true;
       int jt = 0;
-      while (ok && walk.next(seg)) {
+      for (int nseg = 0; ok && segment(nseg); ++nseg) {
         const int first = seg.ctx - seg.L;
         for (int j = seg.j0; j < seg.j1; ++j, ++jt) {
           const int slot = jt % VS, rs = jt % RS, t0 = j * kTileKeys;
@@ -934,74 +1011,48 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
 // Joins the parts of a (sequence, KV head, row tile) whose key tiles several CTAs ran: part 0
 // is the last segment of CTA b, part k > 0 the first segment of CTA b + k.
 //   M = max lse_k,  out = sum_k 2^(lse_k - M) o_k / sum_k 2^(lse_k - M)
-// A warp per row; the parts' results were just written and come from L2.
-constexpr int kMergeWarps = 8;
+// A thread has one row and four head-dim columns, a warp 32 adjacent rows: its loads are whole
+// lines, just written and still in L2.
+constexpr int kMergeThreads = 256, kMergeSplit = 8;
 template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
-  constexpr int PER = D / 32;
+__global__ void __launch_bounds__(kMergeThreads)
+    tree_merge_kernel(const __grid_constant__ TreeArgs a) {
   pdl_trigger();
   pdl_wait();
-  const int b = blockIdx.x, lane = threadIdx.x & 31;
-  const int4 it = a.join[b];
-  if (it.w == 0) return;
-  const int t = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
-  const SeqInfo i = seq_info(a, it.x, false);
-  const int r = it.z * kTileRows + t, G = a.group;
-  if (r >= i.L * G) return;
-  auto part = [&](int k) {
-    return ((size_t)(b + k) * 2 + (k == 0 ? 1 : 0)) * kTileRows + t;
-  };
-  float M = -INFINITY, L = 0.f, acc[PER];
-#pragma unroll
-  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-  for (int k0 = 0; k0 < it.w; k0 += 32) {
-    const int n = min(32, it.w - k0);
-    const float x = lane < n ? __ldcg(a.part_lse + part(k0 + lane)) : -INFINITY;
-    float mb = x;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) mb = fmaxf(mb, __shfl_xor_sync(kFullMask, mb, off));
-    const float mn = fmaxf(M, mb), ref = mn == -INFINITY ? 0.f : mn;
-    const float sc = M == -INFINITY ? 0.f : exp2f(M - ref);
-    M = mn;
-    const float w = lane < n ? exp2f(x - ref) : 0.f;
-    float ws = w;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) ws += __shfl_xor_sync(kFullMask, ws, off);
-    L = fmaf(L, sc, ws);
-#pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] *= sc;
-    for (int k = 0; k < n; k += 8) {
-      float v[8][PER];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        if (k + u >= n) continue;
-        const float *src = a.part_o + part(k0 + k + u) * D + lane * PER;
-        if constexpr (PER == 4) {
-          const float4 f = __ldcg(reinterpret_cast<const float4 *>(src));
-          v[u][0] = f.x, v[u][1] = f.y, v[u][2] = f.z, v[u][3] = f.w;
-        } else {
-          const float2 f = __ldcg(reinterpret_cast<const float2 *>(src));
-          v[u][0] = f.x, v[u][1] = f.y;
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        if (k + u >= n) continue;
-        const float c = __shfl_sync(kFullMask, w, k + u);
-        // a part that saw nothing, or whose weight vanishes, adds nothing
-        if (c != 0.f)
-#pragma unroll
-          for (int e = 0; e < PER; ++e) acc[e] = fmaf(c, v[u][e], acc[e]);
-      }
+  const int b = blockIdx.x;
+  const TreeJoin it = a.join[b];
+  if (it.parts == 0) return;
+  const int G = a.group, rows = min(it.rows - it.m * kTileRows, kTileRows);
+  const int t = threadIdx.x & (kTileRows - 1);
+  if (t >= rows) return;
+  const int r = it.m * kTileRows + t;
+  // part k's first slot: CTA b's second, then the first of the CTAs after it
+  const float *lse = a.part_lse + (size_t)(2 * b) * kTileRows + t;
+  auto slot = [&](int k) { return 2 * k + (k == 0 ? 1 : 0); };
+  float M = -INFINITY;
+#pragma unroll 1
+  for (int k = 0; k < it.parts; ++k) M = fmaxf(M, __ldcg(lse + slot(k) * kTileRows));
+  const float ref = M == -INFINITY ? 0.f : M;
+  uint16_t *out = a.out + ((size_t)(it.q0 + r / G) * a.q_heads + it.g * G + r % G) * D;
+  constexpr int kStep = kMergeThreads / kTileRows;
+#pragma unroll 1
+  for (int c = blockIdx.y * kStep + threadIdx.x / kTileRows; c < D / 4; c += gridDim.y * kStep) {
+    const float4 *src = a.part_o + ((size_t)(2 * b) * (D / 4) + c) * kTileRows + t;
+    float L = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < it.parts; ++k) {
+      const float w = exp2f(__ldcg(lse + slot(k) * kTileRows) - ref);
+      const float4 v = __ldcg(src + (size_t)slot(k) * (D / 4) * kTileRows);
+      L += w;
+      // a part that saw nothing, or whose weight vanishes, adds nothing
+      if (w != 0.f)
+        o = make_float4(fmaf(w, v.x, o.x), fmaf(w, v.y, o.y), fmaf(w, v.z, o.z), fmaf(w, v.w, o.w));
     }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    *reinterpret_cast<uint2 *>(out + 4 * c) =
+        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
   }
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  uint16_t *o = a.out + ((size_t)(i.q0 + r / G) * a.q_heads + it.y * G + r % G) * D + lane * PER;
-  if constexpr (PER == 4)
-    *reinterpret_cast<uint2 *>(o) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv),
-                                               pack_bf16(acc[2] * inv, acc[3] * inv));
-  else
-    *reinterpret_cast<uint32_t *>(o) = pack_bf16(acc[0] * inv, acc[1] * inv);
 }
 
 // Workspace: join records, then the parts' log-sum-exps and outputs.
@@ -1014,7 +1065,7 @@ TreeWorkspace tree_workspace(int group, int head_dim, int max_query_len) {
   const int64_t tiles = ((int64_t)max_query_len * group + kTileRows - 1) / kTileRows;
   w.ctas = 2 * device_sm_count() + (tiles < kMaxRowTiles ? tiles : kMaxRowTiles);
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-  w.lse_off = up(w.ctas * sizeof(int4));
+  w.lse_off = up(w.ctas * sizeof(TreeJoin));
   w.o_off = up(w.lse_off + w.ctas * 2 * kTileRows * sizeof(float));
   w.total = up(w.o_off + w.ctas * 2 * kTileRows * (size_t)head_dim * sizeof(float));
   return w;
@@ -1047,8 +1098,7 @@ int launch_tree(TreeArgs a, int64_t tiles, int64_t ctas, const CUtensorMap &tk,
     if ((int64_t)grid > ctas) return PKV_ERR_WORKSPACE;
     if (launch_pdl(tree_attention_kernel<D, F8>, dim3(grid), dim3(tree_threads(F8)),
                    (size_t)Lay::kSmemLaunch, st, a, tk, tv) != cudaSuccess ||
-        launch_pdl(tree_merge_kernel<D>, dim3(grid, kTileRows / kMergeWarps),
-                   dim3(kMergeWarps * 32), 0, st, a) != cudaSuccess)
+        launch_pdl(tree_merge_kernel<D>, dim3(grid, kMergeSplit), dim3(kMergeThreads), 0, st, a) != cudaSuccess)
       return PKV_ERR_CUDA;
   }
   return PKV_OK;
@@ -1092,9 +1142,9 @@ int tree_impl(uint16_t *out, const uint16_t *q, const void *k_cache, const void 
   a.v_scale = v_scale;
   a.k_scales = k_scales, a.v_scales = v_scales;
   char *wb = static_cast<char *>(workspace);
-  a.join = reinterpret_cast<int4 *>(wb);
+  a.join = reinterpret_cast<TreeJoin *>(wb);
   a.part_lse = reinterpret_cast<float *>(wb + ws.lse_off);
-  a.part_o = reinterpret_cast<float *>(wb + ws.o_off);
+  a.part_o = reinterpret_cast<float4 *>(wb + ws.o_off);
   a.err = err_flag;
   CUtensorMap tk = {}, tv = {};
   const uint64_t rows = (uint64_t)num_blocks * num_kv_heads * kBlockSize;
