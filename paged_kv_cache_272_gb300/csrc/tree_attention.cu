@@ -308,22 +308,19 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t *>(&h);
 }
-// Four values -> their E4M3 codes, and what is left of the values.
-__device__ __forceinline__ uint32_t e4m3_split(float (&x)[4]) {
-  uint32_t c[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    c[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i], x[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-    const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c[i], __NV_E4M3));
-    x[2 * i] -= __low2float(h);
-    x[2 * i + 1] -= __high2float(h);
-  }
-  return (c[0] & 0xffffu) | (c[1] << 16);
+// Two f16 values -> their E4M3 codes (low 16 bits), and exactly what is left of the values.
+__device__ __forceinline__ uint32_t e4m3_split(__half2 &x) {
+  const uint32_t c = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
+  x = __hsub2(x, __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c, __NV_E4M3)));
+  return c & 0xffffu;
 }
 // Two E4M3 codes (low 16 bits) -> two f16, exact.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t c) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xffffu), __NV_E4M3);
   return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {  // bit 7 of each NaN code's byte
+  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 __device__ __forceinline__ float e4m3_to_f32(uint8_t c) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
@@ -499,42 +496,46 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
         // largest element in [128, 256): q1 takes 4 significant bits and q2 the other 4 of
         // bf16's 8, exactly for elements down to 2^-9 of the largest, and to 2^-10 absolute
         // below.  q1 goes to TMEM (four codes per column), q2 to shared memory (D 64: TMEM).
-        uint32_t big = 0;  // largest magnitude, as bf16 bits
-#pragma unroll 1
-        for (int half = 0; half < H; ++half) {
-          uint4 v[8];
+        uint4 v[8 * H];  // every load before the first use
 #pragma unroll
-          for (int c = 0; c < 8; ++c) v[c] = valid ? qrow[8 * half + c] : make_uint4(0u, 0u, 0u, 0u);
+        for (int c = 0; c < 8 * H; ++c) v[c] = valid ? qrow[c] : make_uint4(0u, 0u, 0u, 0u);
+        __nv_bfloat162 big = __float2bfloat162_rn(0.f);  // largest magnitudes (a NaN stays)
+        auto grow = [&](uint32_t w) {
+          big = __hmax2_nan(big, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w)));
+        };
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            big = __vmaxu2(big, __vmaxu2(v[c].x & 0x7fff7fffu, v[c].y & 0x7fff7fffu));
-            big = __vmaxu2(big, __vmaxu2(v[c].z & 0x7fff7fffu, v[c].w & 0x7fff7fffu));
-          }
-        }
-        const int bits = max(big & 0xffffu, big >> 16);
+        for (int c = 0; c < 8 * H; ++c) grow(v[c].x), grow(v[c].y), grow(v[c].z), grow(v[c].w);
+        const uint32_t bb = *reinterpret_cast<const uint32_t *>(&big) & 0x7fff7fffu;
+        const int bits = max(bb & 0xffffu, bb >> 16);
         const bool odd = bits >= 0x7f80;  // an infinity or NaN: no finite score in this row
         const int e = odd || bits == 0 ? 0 : min(134 - (bits >> 7), 120);
         const float up = __uint_as_float((uint32_t)(127 + e) << 23);
         sl *= __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll 1
-        for (int c = 0; c < 4 * H; ++c) {  // 16 elements
-          uint32_t q1[4], q2[4];
-          const uint4 v0 = valid ? qrow[2 * c] : make_uint4(0u, 0u, 0u, 0u);
-          const uint4 v1 = valid ? qrow[2 * c + 1] : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        for (int c = 0; c < 2 * H; ++c) {  // 32 elements; the row moves down by as many
+          uint32_t q1[8], q2[8];
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            float x[4] = {bf16_lo(w[2 * h]) * up, bf16_hi(w[2 * h]) * up,
-                          bf16_lo(w[2 * h + 1]) * up, bf16_hi(w[2 * h + 1]) * up};
-            q1[h] = odd ? ~0u : e4m3_split(x);
-            q2[h] = odd ? ~0u : e4m3_split(x);
+          for (int h = 0; h < 8; ++h) {
+            const uint4 &x4 = v[h >> 1];
+            const uint32_t w0 = h & 1 ? x4.z : x4.x, w1 = h & 1 ? x4.w : x4.y;
+            // f16 holds q 2^e exactly where q1 + q2 can (down to 2^-17)
+            __half2 x0 = __floats2half2_rn(bf16_lo(w0) * up, bf16_hi(w0) * up);
+            __half2 x1 = __floats2half2_rn(bf16_lo(w1) * up, bf16_hi(w1) * up);
+            q1[h] = e4m3_split(x0), q1[h] |= e4m3_split(x1) << 16;
+            q2[h] = e4m3_split(x0), q2[h] |= e4m3_split(x1) << 16;
+            if (odd) q1[h] = ~0u;
           }
-          tmem_st4(tQ + 4 * c + lane_base, q1);
-          if (H == 1)
-            tmem_st4(tQ + 16 + 4 * c + lane_base, q2);
-          else
-            st_shared_v4(sQ + t * 128 + ((c ^ (t & 7)) << 4),
+#pragma unroll
+          for (int i2 = 0; i2 + 4 < 8 * H; ++i2) v[i2] = v[i2 + 4];
+          tmem_st8(tQ + 8 * c + lane_base, q1);
+          if (H == 1) {
+            tmem_st8(tQ + 16 + 8 * c + lane_base, q2);
+          } else {
+            st_shared_v4(sQ + t * 128 + (((2 * c) ^ (t & 7)) << 4),
                          make_uint4(q2[0], q2[1], q2[2], q2[3]));
+            st_shared_v4(sQ + t * 128 + (((2 * c + 1) ^ (t & 7)) << 4),
+                         make_uint4(q2[4], q2[5], q2[6], q2[7]));
+          }
         }
       }
       wait_st();
@@ -705,24 +706,29 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
 #pragma unroll 1
         for (int half = 0; half < H; ++half) {
 #pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            uint32_t o[8];
-            tmem_ld8(tO + 64 * half + 8 * c + lane_base, o);
+          for (int cc = 0; cc < 2; ++cc) {
+            uint32_t o[32];
+            tmem_ld32(tO + 64 * half + 32 * cc + lane_base, o);
             wait_ld();
-            uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-            st_shared_v4(stage + ((c ^ (t & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+            for (int c = 0; c < 4; ++c) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i2 = 0; i2 < 4; ++i2)
+                w[i2] = pack_bf16(__uint_as_float(o[8 * c + 2 * i2]) * inv,
+                                  __uint_as_float(o[8 * c + 2 * i2 + 1]) * inv);
+              st_shared_v4(stage + (((4 * cc + c) ^ (t & 7)) << 4),
+                           make_uint4(w[0], w[1], w[2], w[3]));
+            }
           }
           __syncwarp();
+          int rr = warp * 32 + (lane >> 3), tok = (r0 + rr) / G, head = (r0 + rr) - tok * G;
 #pragma unroll 1
-          for (int it = 0; it < 8; ++it) {
-            const int rr = warp * 32 + it * 4 + (lane >> 3), c = lane & 7, ro = r0 + rr;
-            if (ro < rows)
-              *reinterpret_cast<uint4 *>(
-                  a.out + ((size_t)(seg.q0 + ro / G) * a.q_heads + seg.g * G + ro % G) * D +
-                  64 * half + 8 * c) = ld_shared_v4(sQ + rr * 128 + ((c ^ (rr & 7)) << 4));
+          for (; rr < warp * 32 + 32 && r0 + rr < rows; rr += 4) {
+            *reinterpret_cast<uint4 *>(
+                a.out + ((size_t)(seg.q0 + tok) * a.q_heads + seg.g * G + head) * D + 64 * half +
+                8 * (lane & 7)) = ld_shared_v4(sQ + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+            for (head += 4; head >= G; head -= G) ++tok;
           }
           __syncwarp();
         }
@@ -730,14 +736,14 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
         if (valid) a.part_lse[part] = l == 0.f ? -INFINITY : m + log2f(l);
         float4 *dst = a.part_o + (part - t) * (D / 4) + t;
 #pragma unroll 1
-        for (int c = 0; c < D / 8; ++c) {
-          uint32_t o[8];
-          tmem_ld8(tO + 8 * c + lane_base, o);
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t o[32];
+          tmem_ld32(tO + 32 * cc + lane_base, o);
           wait_ld();
           if (valid)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              dst[(2 * c + e) * kTileRows] =
+            for (int e = 0; e < 8; ++e)
+              dst[(8 * cc + e) * kTileRows] =
                   make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
                               __uint_as_float(o[4 * e + 2]) * inv,
                               __uint_as_float(o[4 * e + 3]) * inv);
@@ -961,17 +967,20 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
           if (__builtin_expect(t0 + kTileKeys > first, 0)) {
             // a tile of the tree: keys past the context, and values that are not finite,
             // become zero
+            auto bytes_below = [](int n) {  // a mask of a word's first n bytes
+              return n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
+            };
 #pragma unroll 1
             for (int it = 0; it < kSteps; ++it) {
               uint4 v = ld_shared_v4(src + it * 2048);
-              const int key0 = t0 + (it * 128 + e0) / D * kBlockSize;
-#pragma unroll 1
-              for (int b = 0; b < kBlockSize; ++b) {
-                uint32_t &w = b < 8 ? (b < 4 ? v.x : v.y) : (b < 12 ? v.z : v.w);
-                const uint32_t m = 0x7fu << (8 * (b & 3)), key = key0 + b;
-                const bool nan = (w & m) == m && (int)key >= first && (int)key < seg.ctx;
-                if (nan || (int)key >= seg.ctx) w &= ~(0xffu << (8 * (b & 3)));
-                hit |= nan;
+              int key = t0 + (it * 128 + e0) / D * kBlockSize;
+              uint32_t *w = &v.x;
+#pragma unroll
+              for (int q = 0; q < 4; ++q, key += 4) {
+                const uint32_t held = bytes_below(seg.ctx - key);
+                const uint32_t nan = nan_codes(w[q]) & held & ~bytes_below(first - key);
+                hit |= nan != 0;
+                w[q] &= held & ~((nan >> 7) * 0xffu);
               }
               st_shared_v4(src + it * 2048, v);
             }
