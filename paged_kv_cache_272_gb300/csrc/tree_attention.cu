@@ -63,6 +63,10 @@ constexpr int kLaunchRegs = 80, kSoftmaxRegs = 128, kOtherRegs = 56;
 static_assert(128 * kSoftmaxRegs + 256 * kOtherRegs <= 384 * kLaunchRegs, "register split");
 constexpr uint32_t kTmemColumns = 256;
 constexpr int kMaxRowTiles = 64;  // row tiles of one launch
+// A segment's start and finish, in key tiles.  Measured, none / 4 / 8 / 12: 32 ragged sequences
+// 79.1 / 77.4 / 77.0 / 78.3 us, short MHA contexts 29.4 / 27.8 / 29.2 / 29.3; E4M3, 64 ragged
+// sequences 186 / 180 / 176 / 176 (q's two terms take longer to make).
+constexpr int kStart = 5, kStartF8 = 8;
 
 struct TreeArgs {
   uint16_t *out;                // [T][Hq][D] bf16
@@ -78,6 +82,7 @@ struct TreeArgs {
   float v_scale;
   const float *k_scales, *v_scales;  // [Hkv] or null
   int runs;                     // CTAs that share the key tiles
+  int start;                    // what a segment costs besides its tiles, in tiles
   int m0, row_tiles;            // this launch's row tiles m0 .. m0 + row_tiles - 1
   struct TreeJoin *join;        // [CTAs] what starts and does not end in a CTA
   float *part_lse;              // [CTAs][2][128] log2-sum-exp2
@@ -113,13 +118,16 @@ __device__ __forceinline__ SeqInfo seq_info(const TreeArgs &a, int s, bool flag)
   return i;
 }
 
-// A CTA's run of key tiles, filled by plan_run.
+// A CTA's run, filled by plan_run.  Runs are cut in units: a (sequence, KV head) pair is as
+// many as it has key tiles and a.start more at its beginning, which stand for the time that
+// any segment takes to start and finish (Q, first scores, last product, output).  A run that
+// meets many short pairs so gets fewer tiles.
 struct Plan {
-  unsigned long long tiles[kMaxRowTiles];  // key tiles of row tile m (all KV heads); later the
+  unsigned long long tiles[kMaxRowTiles];  // units of row tile m (all KV heads); later the
                                            // ring of segments
   unsigned long long warp_sum[tree_threads(true) / 32];
-  unsigned long long off;  // first tile within sequence s (KV heads end to end)
-  long long left;          // tiles of the run
+  unsigned long long off;  // first unit within sequence s (KV heads end to end)
+  long long left;          // units of the run
   long long cta_tiles, extra;  // run length of this row tile's CTAs: cta_tiles, one more for
   int ctas, cta;               // the first `extra` of its `ctas`; this CTA's number there
   int s, m;
@@ -146,8 +154,8 @@ __device__ __forceinline__ void plan_run(const TreeArgs &a, Plan *p) {
     const SeqInfo i = seq_info(a, s, blockIdx.x == 0);
     const int last = min(i.row_tiles - a.m0, a.row_tiles);
     if (i.tiles == 0 || last <= 0) continue;
-    mine += i.tiles;
-    if (!one) atomicAdd(&p->tiles[last - 1], (unsigned long long)i.tiles);
+    mine += i.tiles + a.start;
+    if (!one) atomicAdd(&p->tiles[last - 1], (unsigned long long)(i.tiles + a.start));
   }
   if (one) {
 #pragma unroll 1
@@ -206,7 +214,8 @@ __device__ __forceinline__ void plan_run(const TreeArgs &a, Plan *p) {
     unsigned long long n = 0;
     if (s < a.num_seqs) {
       const SeqInfo i = seq_info(a, s, false);
-      if (i.row_tiles > m) n = (unsigned long long)i.tiles * a.kv_heads;
+      if (i.tiles > 0 && i.row_tiles > m)
+        n = (unsigned long long)(i.tiles + a.start) * a.kv_heads;
     }
     unsigned long long incl = n;
 #pragma unroll 1
@@ -247,32 +256,36 @@ static_assert(kSegRing * sizeof(Segment) <= kMaxRowTiles * sizeof(unsigned long 
 struct Walk {
   const TreeArgs &a;
   long long left;
-  int m, s, g, tile;
+  int m, s, g, unit;
   SeqInfo i;
   __device__ Walk(const TreeArgs &args, const Plan &p)
-      : a(args), left(p.left), m(p.m), s(p.s), g(0), tile(0) {
-    if (left > 0) {
-      i = seq_info(a, s, false);
-      g = (int)(p.off / i.tiles);
-      tile = (int)(p.off % i.tiles);
+      : a(args), left(p.left), m(p.m), s(p.s), g(0), unit(0) {
+    i = seq_info(a, s, false);
+    const unsigned n = (unsigned)(i.tiles + a.start);
+    if (p.off >> 32) {
+      g = (int)(p.off / n), unit = (int)(p.off % n);
+    } else {
+      g = (int)((unsigned)p.off / n), unit = (int)((unsigned)p.off % n);
     }
   }
   __device__ bool next(Segment &o) {
-    if (left <= 0) return false;
-    if (g == a.kv_heads) {
-      g = 0;
-      do {
-        if (++s >= a.num_seqs) return false;  // not reached: the run's tiles are counted
-        i = seq_info(a, s, false);
-      } while (i.tiles == 0 || i.row_tiles <= m);
+    while (left > 0) {
+      if (g == a.kv_heads) {
+        g = 0;
+        do {
+          if (++s >= a.num_seqs) return false;  // not reached: the run's units are counted
+          i = seq_info(a, s, false);
+        } while (i.tiles == 0 || i.row_tiles <= m);
+      }
+      const int end = (int)min((long long)(i.tiles + a.start), unit + left);
+      left -= end - unit;
+      o.s = s, o.g = g, o.q0 = i.q0, o.L = i.L, o.ctx = i.ctx, o.tiles = i.tiles;
+      o.j0 = max(unit - a.start, 0), o.j1 = max(end - a.start, 0);
+      unit = 0;
+      ++g;
+      if (o.j1 > o.j0) return true;
     }
-    o.s = s, o.g = g, o.q0 = i.q0, o.L = i.L, o.ctx = i.ctx, o.tiles = i.tiles;
-    o.j0 = tile;
-    o.j1 = (int)min((long long)i.tiles, tile + left);
-    left -= o.j1 - o.j0;
-    tile = 0;
-    ++g;
-    return true;
+    return false;
   }
 };
 
@@ -1100,6 +1113,7 @@ int launch_tree(TreeArgs a, int64_t tiles, int64_t ctas, const CUtensorMap &tk,
   });
   if (r <= 0) return PKV_ERR_CUDA;
   a.runs = 2 * device_sm_count();
+  a.start = F8 ? kStartF8 : kStart;
   for (int64_t m0 = 0; m0 < tiles; m0 += kMaxRowTiles) {
     a.m0 = (int)m0;
     a.row_tiles = (int)(tiles - m0 < kMaxRowTiles ? tiles - m0 : kMaxRowTiles);
