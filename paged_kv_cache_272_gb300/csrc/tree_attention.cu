@@ -67,6 +67,9 @@ constexpr int kMaxRowTiles = 64;  // row tiles of one launch
 // 79.1 / 77.4 / 77.0 / 78.3 us, short MHA contexts 29.4 / 27.8 / 29.2 / 29.3; E4M3, 64 ragged
 // sequences 186 / 180 / 176 / 176 (q's two terms take longer to make).
 constexpr int kStart = 5, kStartF8 = 8;
+// Least units of a run: one sequence of 700 tokens takes 20.1 us with runs of one unit, 17.0
+// with 2, 15.2 with 4 (fewer parts to join), 16.5 with 6.
+constexpr int kMinRun = 4;
 
 struct TreeArgs {
   uint16_t *out;                // [T][Hq][D] bf16
@@ -182,7 +185,7 @@ __device__ __forceinline__ void plan_run(const TreeArgs &a, Plan *p) {
     for (int m = 0; m < a.row_tiles && p->tiles[m]; ++m) {
       const unsigned long long w = p->tiles[m];
       int n = one ? a.runs : share(a.runs, w, total);
-      if ((unsigned long long)n > w) n = (int)w;
+      if ((unsigned long long)n > (w + kMinRun - 1) / kMinRun) n = (int)((w + kMinRun - 1) / kMinRun);
       if (n < 1) n = 1;
       const int c = (int)blockIdx.x - at;
       if (c < n) {
@@ -1033,9 +1036,10 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
 // Joins the parts of a (sequence, KV head, row tile) whose key tiles several CTAs ran: part 0
 // is the last segment of CTA b, part k > 0 the first segment of CTA b + k.
 //   M = max lse_k,  out = sum_k 2^(lse_k - M) o_k / sum_k 2^(lse_k - M)
-// A thread has one row and four head-dim columns, a warp 32 adjacent rows: its loads are whole
-// lines, just written and still in L2.
-constexpr int kMergeThreads = 256, kMergeSplit = 8;
+// A thread has one row and four head-dim columns at a time, a warp 32 adjacent rows: its loads
+// are whole lines, just written and still in L2.  Four parts at a time, so that the common
+// two or three cost one round trip for the weights and one for the values.
+constexpr int kMergeThreads = 256, kMergeSplit = 4;
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads)
     tree_merge_kernel(const __grid_constant__ TreeArgs a) {
@@ -1048,28 +1052,46 @@ __global__ void __launch_bounds__(kMergeThreads)
   const int t = threadIdx.x & (kTileRows - 1);
   if (t >= rows) return;
   const int r = it.m * kTileRows + t;
-  // part k's first slot: CTA b's second, then the first of the CTAs after it
+  // part 0 is CTA b's second slot, part k > 0 the first of CTA b + k
   const float *lse = a.part_lse + (size_t)(2 * b) * kTileRows + t;
   auto slot = [&](int k) { return 2 * k + (k == 0 ? 1 : 0); };
-  float M = -INFINITY;
+  auto lse_of = [&](int k) {
+    return k < it.parts ? __ldcg(lse + slot(k) * kTileRows) : -INFINITY;
+  };
+  float M = -INFINITY, x[4];
 #pragma unroll 1
-  for (int k = 0; k < it.parts; ++k) M = fmaxf(M, __ldcg(lse + slot(k) * kTileRows));
+  for (int k = (it.parts - 1) & ~3; k >= 0; k -= 4) {  // the first four last: they stay in x
+#pragma unroll
+    for (int u = 0; u < 4; ++u) x[u] = lse_of(k + u);
+    M = fmaxf(M, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+  }
   const float ref = M == -INFINITY ? 0.f : M;
   uint16_t *out = a.out + ((size_t)(it.q0 + r / G) * a.q_heads + it.g * G + r % G) * D;
   constexpr int kStep = kMergeThreads / kTileRows;
-#pragma unroll 1
-  for (int c = blockIdx.y * kStep + threadIdx.x / kTileRows; c < D / 4; c += gridDim.y * kStep) {
+#pragma unroll 2
+  for (int c = blockIdx.y * kStep + threadIdx.x / kTileRows; c < D / 4; c += kMergeSplit * kStep) {
     const float4 *src = a.part_o + ((size_t)(2 * b) * (D / 4) + c) * kTileRows + t;
     float L = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = 0; k < it.parts; ++k) {
-      const float w = exp2f(__ldcg(lse + slot(k) * kTileRows) - ref);
-      const float4 v = __ldcg(src + (size_t)slot(k) * (D / 4) * kTileRows);
-      L += w;
-      // a part that saw nothing, or whose weight vanishes, adds nothing
-      if (w != 0.f)
-        o = make_float4(fmaf(w, v.x, o.x), fmaf(w, v.y, o.y), fmaf(w, v.z, o.z), fmaf(w, v.w, o.w));
+#pragma unroll 1
+    for (int k = 0; k < it.parts; k += 4) {
+      float4 v[4];
+      float w[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k + u < it.parts) v[u] = __ldcg(src + (size_t)slot(k + u) * (D / 4) * kTileRows);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) w[u] = exp2f((k == 0 ? x[u] : lse_of(k + u)) - ref);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        L += w[u];
+        // a part that saw nothing, or whose weight vanishes, adds nothing
+        if (w[u] != 0.f)
+          o = make_float4(fmaf(w[u], v[u].x, o.x), fmaf(w[u], v[u].y, o.y),
+                          fmaf(w[u], v[u].z, o.z), fmaf(w[u], v[u].w, o.w));
+      }
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
     *reinterpret_cast<uint2 *>(out + 4 * c) =
