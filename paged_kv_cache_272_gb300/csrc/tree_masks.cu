@@ -8,9 +8,11 @@
 // ceil(log2(depth + 1)) rounds of  row(i) |= row(jump(i)), jump(i) = jump(jump(i))  finish
 // any tree.  The bytes are a few per token; the time is the launch and two dependent reads.
 //
-// Commit.  Each (sequence, KV head, cache, 128-byte slice of the rows) is one CTA that reads
-// every accepted row into shared memory, waits, and writes them out, so a path may overlap
-// the slots it moves to.  Latency-bound: lengths, path, slots, rows are dependent reads.
+// Commit.  A unit is one (KV head, cache, 128-byte slice of the rows) of a sequence.  A CTA
+// reads the accepted rows of up to eight units, a warp each, into shared memory, waits, and
+// writes them out, so a path may overlap the slots it moves to.  Latency-bound: lengths, path,
+// slots and rows are dependent reads, so the rows of a warp are read in batches and the CTAs
+// fit in one wave (one unit each, 200 sequences x 16 heads of an E4M3 cache were 6400 CTAs).
 #include "pkv_common.cuh"
 
 namespace pkv {
@@ -77,21 +79,22 @@ struct CommitArgs {
   const int64_t *dst_slots; // [S][A] or null (the sequence's own first slots)
   const int32_t *query_start, *accepted, *accepted_lens;
   int num_tokens, max_accept, heads, head_dim, elem;
+  int slices, units;        // slices of a row; units of a sequence (2 * heads * slices)
+  int per_cta;              // units of a CTA: 8, 4, 2 or 1
   int64_t num_slots;
   int v_transposed;         // E4M3 V: [D][16] within a block
   int32_t *err;
 };
 
-constexpr int kSlice = 128;         // bytes of a row one CTA moves
-constexpr int kCommitThreads = 128;
+constexpr int kSlice = 128;         // bytes of a row in one unit
+constexpr int kCommitWarps = 8, kCommitThreads = 32 * kCommitWarps;
+constexpr int kCommitSmem = 64 * 1024;  // most a CTA stages when it has several units
 
 __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const CommitArgs a) {
-  extern __shared__ __align__(16) uint8_t stage[];  // [max_accept][kSlice], then slot pairs
+  extern __shared__ __align__(16) uint8_t stage[];  // [per_cta][max_accept][kSlice], slot pairs
   pdl_trigger();
   pdl_wait();
-  const int s = blockIdx.x, h = blockIdx.y;
-  const bool is_v = (blockIdx.z & 1) != 0;
-  const int slice = blockIdx.z >> 1;
+  const int s = blockIdx.x, u0 = blockIdx.y * a.per_cta;
   const int q0 = a.query_start[s], q1 = a.query_start[s + 1], n = a.accepted_lens[s];
   if (n == 0) return;
   const int64_t L = (int64_t)q1 - q0;
@@ -101,7 +104,8 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const Commi
     return;
   }
   // Source and destination slots of the accepted rows, once per CTA (-1: not moved).
-  int64_t *const ss = reinterpret_cast<int64_t *>(stage + (size_t)a.max_accept * kSlice);
+  int64_t *const ss =
+      reinterpret_cast<int64_t *>(stage + (size_t)a.per_cta * a.max_accept * kSlice);
   for (int r = threadIdx.x; r < n; r += kCommitThreads) {
     const int idx = a.accepted[(size_t)s * a.max_accept + r];
     int64_t src = -1, dst = -1;
@@ -119,36 +123,96 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const Commi
     ss[2 * r + 1] = dst;
   }
   __syncthreads();
-  uint8_t *cache = is_v ? a.v_cache : a.k_cache;
+  // Warps of one unit share its rows.
+  const int wpu = kCommitWarps / a.per_cta, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int k = warp / wpu, sub = warp % wpu, u = u0 + k;
+  const bool on = u < a.units;
+  const int slice = u % a.slices, hc = u / a.slices, h = hc >> 1;
+  const bool is_v = (hc & 1) != 0;
+  uint8_t *const cache = is_v ? a.v_cache : a.k_cache;
+  uint8_t *const st = stage + (size_t)k * a.max_accept * kSlice;
+  constexpr int kBatch = 4;  // rows in flight
+  const bool bytes = is_v && a.v_transposed;
+  // Transposed V: lane d owns head-dim rows d, d + 32, ... of the block, one byte per token.
+  constexpr int kMost = 128 / 32;
+  auto byte_at = [&](int64_t slot) {
+    return cache + (((slot >> 4) * a.heads + h) * a.head_dim + lane) * kBlockSize + (slot & 15);
+  };
+  // The others: 16-byte vectors, several rows side by side.
   const int64_t row_bytes = (int64_t)a.head_dim * a.elem;
-  if (is_v && a.v_transposed) {
-    // thread d owns head-dim row d of the block: one byte per token
-    const int d = threadIdx.x;
-    auto at = [&](int64_t slot) {
-      return cache + (((slot >> 4) * a.heads + h) * a.head_dim + d) * kBlockSize + (slot & 15);
-    };
-    if (d >= a.head_dim) return;  // no thread reads another's bytes
-#pragma unroll 8
-    for (int r = 0; r < n; ++r)
-      if (ss[2 * r] >= 0) stage[r * kSlice + d] = *at(ss[2 * r]);
-    for (int r = 0; r < n; ++r)
-      if (ss[2 * r] >= 0) *at(ss[2 * r + 1]) = stage[r * kSlice + d];
-    return;
-  }
   const int lanes = row_bytes < kSlice ? (int)(row_bytes / 16) : kSlice / 16;
-  const int e = threadIdx.x % lanes, step = kCommitThreads / lanes;
-  auto at = [&](int64_t slot) {
+  const int e = lane % lanes, per = 32 / lanes, first = sub * per + lane / lanes;
+  const int step = wpu * per;
+  auto vec_at = [&](int64_t slot) {
     return reinterpret_cast<uint4 *>(
         cache + (((slot >> 4) * a.heads + h) * kBlockSize + (slot & 15)) * row_bytes +
         slice * kSlice + e * 16);
   };
-  uint4 *st = reinterpret_cast<uint4 *>(stage);
-#pragma unroll 4
-  for (int r = threadIdx.x / lanes; r < n; r += step)
-    if (ss[2 * r] >= 0) st[r * (kSlice / 16) + e] = *at(ss[2 * r]);
+  uint4 *const sv = reinterpret_cast<uint4 *>(st) + e;
+  if (on && bytes) {
+    for (int r0 = sub * kBatch; r0 < n; r0 += wpu * kBatch) {
+      uint8_t v[kBatch][kMost];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+        if (r0 + b < n && ss[2 * (r0 + b)] >= 0)
+#pragma unroll
+          for (int j = 0; j < kMost; ++j)
+            if (32 * j < a.head_dim) v[b][j] = byte_at(ss[2 * (r0 + b)])[32 * j * kBlockSize];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+        if (r0 + b < n && ss[2 * (r0 + b)] >= 0)
+#pragma unroll
+          for (int j = 0; j < kMost; ++j)
+            if (32 * j < a.head_dim) st[(r0 + b) * kSlice + lane + 32 * j] = v[b][j];
+    }
+  } else if (on) {
+    for (int r0 = first; r0 < n; r0 += step * kBatch) {
+      uint4 v[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int r = r0 + b * step;
+        if (r < n && ss[2 * r] >= 0) v[b] = *vec_at(ss[2 * r]);
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int r = r0 + b * step;
+        if (r < n && ss[2 * r] >= 0) sv[r * (kSlice / 16)] = v[b];
+      }
+    }
+  }
   __syncthreads();
-  for (int r = threadIdx.x / lanes; r < n; r += step)
-    if (ss[2 * r] >= 0) *at(ss[2 * r + 1]) = st[r * (kSlice / 16) + e];
+  if (on && bytes) {
+    // four rows that fill an aligned word of the block leave as one
+    auto word_at = [&](int r) {
+      if (r + 3 >= n) return false;
+      const int64_t dst = ss[2 * r + 1];
+      bool ok = (dst & 3) == 0;
+      for (int i = 0; i < 4; ++i) ok = ok && ss[2 * (r + i)] >= 0 && ss[2 * (r + i) + 1] == dst + i;
+      return ok;
+    };
+    const int share = (n + wpu - 1) / wpu, end = min(n, (sub + 1) * share);
+    for (int r = sub * share; r < end;) {
+      const bool word = r + 3 < end && word_at(r);
+      if (ss[2 * r] >= 0) {
+        uint8_t *dst = byte_at(ss[2 * r + 1]);
+        const uint8_t *src = st + r * kSlice + lane;
+#pragma unroll
+        for (int j = 0; j < kMost; ++j)
+          if (32 * j < a.head_dim) {
+            if (word)
+              *reinterpret_cast<uint32_t *>(dst + 32 * j * kBlockSize) =
+                  src[32 * j] | (uint32_t)src[32 * j + kSlice] << 8 |
+                  (uint32_t)src[32 * j + 2 * kSlice] << 16 | (uint32_t)src[32 * j + 3 * kSlice] << 24;
+            else
+              dst[32 * j * kBlockSize] = src[32 * j];
+          }
+      }
+      r += word ? 4 : 1;
+    }
+  } else if (on) {
+    for (int r = first; r < n; r += step)
+      if (ss[2 * r] >= 0) *vec_at(ss[2 * r + 1]) = sv[r * (kSlice / 16)];
+  }
 }
 
 int commit_impl(void *k_cache, void *v_cache, const int64_t *slot_mapping,
@@ -158,7 +222,7 @@ int commit_impl(void *k_cache, void *v_cache, const int64_t *slot_mapping,
                 int32_t *err_flag, void *stream) {
   if (block_size != kBlockSize) return PKV_ERR_BLOCK_SIZE;
   if (num_seqs < 0 || num_tokens < 0 || max_accept < 0 || max_accept > PKV_TREE_MAX_TOKENS ||
-      num_blocks <= 0 || num_kv_heads <= 0 || num_kv_heads > 65535 ||
+      num_blocks <= 0 || num_kv_heads <= 0 || num_kv_heads > 16383 ||
       (head_dim != 64 && head_dim != 128))
     return PKV_ERR_SHAPE;
   if (num_seqs == 0 || num_tokens == 0 || max_accept == 0) return PKV_OK;
@@ -184,16 +248,20 @@ int commit_impl(void *k_cache, void *v_cache, const int64_t *slot_mapping,
   static std::atomic<int> ready[kMaxDevices];
   const int r = per_device_setup(ready, [] {
     return cudaFuncSetAttribute(tree_commit_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                PKV_TREE_MAX_TOKENS * (kSlice + 16)) == cudaSuccess
+                                PKV_TREE_MAX_TOKENS * (kSlice + 16) + kCommitSmem) == cudaSuccess
                ? 1
                : -1;
   });
   if (r <= 0) return PKV_ERR_CUDA;
-  const int slices = (head_dim * elem + kSlice - 1) / kSlice;
+  a.slices = (head_dim * elem + kSlice - 1) / kSlice;
+  a.units = 2 * num_kv_heads * a.slices;
+  a.per_cta = kCommitWarps;
+  while (a.per_cta > 1 && (int64_t)a.per_cta * max_accept * kSlice > kCommitSmem) a.per_cta /= 2;
+  const unsigned ny = (unsigned)((a.units + a.per_cta - 1) / a.per_cta);
+  if (ny > 65535) return PKV_ERR_SHAPE;
   const cudaError_t e = launch_pdl(
-      tree_commit_kernel,
-      dim3((unsigned)num_seqs, (unsigned)num_kv_heads, (unsigned)(2 * slices)),
-      dim3(kCommitThreads), (size_t)max_accept * (kSlice + 16), (cudaStream_t)stream, a);
+      tree_commit_kernel, dim3((unsigned)num_seqs, ny), dim3(kCommitThreads),
+      (size_t)max_accept * ((size_t)a.per_cta * kSlice + 16), (cudaStream_t)stream, a);
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
