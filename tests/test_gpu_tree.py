@@ -276,6 +276,27 @@ def test_attention(ops, case, kind, f8):
 
 
 @pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("lens,Hq,Hkv,D,maxq", [
+    # more sequences than threads of a CTA, most of them shorter than a tile
+    ([(1 + (7 * s) % 90, 1 + (7 * s) % 90 % 3) for s in range(701)], 2, 1, 64, None),
+    # row tiles that only some sequences have
+    ([(260, 70), (300, 3), (129, 129), (40, 1), (64, 64), (900, 33)], 16, 2, 128, None),
+    # more row tiles than one launch takes, for one of two sequences
+    ([(1030, 1024), (80, 5)], 12, 1, 64, None),
+    # many KV heads; a bound on the tree sizes that none reaches
+    ([(100, 5), (33, 9)], 40, 40, 64, 64),
+])
+def test_attention_many_sequences_heads_and_row_tiles(ops, lens, Hq, Hkv, D, maxq, f8):
+    w = Tree(lens, Hq, Hkv, D, seed=len(lens), f8=f8)
+    if maxq:
+        w.maxq = maxq
+    out, d = run_tree(ops, w)
+    ref, bound = w.attention64()
+    assert_within(out, ref, bound)
+    assert int(d["err"]) == 0
+
+
+@pytest.mark.parametrize("f8", [False, True])
 def test_attention_arbitrary_masks(ops, f8):
     """Masks that are no tree: random bits, rows that see nothing of the tree, a whole tree
     with no context and empty rows (zeros), bits past the tree's end, more words than
