@@ -1038,66 +1038,71 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
 // is the last segment of CTA b, part k > 0 the first segment of CTA b + k.
 //   M = max lse_k,  out = sum_k 2^(lse_k - M) o_k / sum_k 2^(lse_k - M)
 // A thread has one row and four head-dim columns at a time, a warp 32 adjacent rows: its loads
-// are whole lines, just written and still in L2.  Four parts at a time, so that the common
-// two or three cost one round trip for the weights and one for the values.
+// are whole lines, just written and still in L2.  What costs is the round trips (the record,
+// then the weights, then the values), so the first two parts' are asked for with the record:
+// where they lie does not depend on it, and most pairs have two or three.
 constexpr int kMergeThreads = 256, kMergeSplit = 4;
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads)
     tree_merge_kernel(const __grid_constant__ TreeArgs a) {
   pdl_trigger();
   pdl_wait();
-  const int b = blockIdx.x;
-  const TreeJoin it = a.join[b];
-  if (it.parts == 0) return;
-  const int G = a.group, rows = min(it.rows - it.m * kTileRows, kTileRows);
-  const int t = threadIdx.x & (kTileRows - 1);
-  if (t >= rows) return;
-  const int r = it.m * kTileRows + t;
+  const int b = blockIdx.x, t = threadIdx.x & (kTileRows - 1);
+  constexpr int kStep = kMergeSplit * (kMergeThreads / kTileRows);
+  constexpr int kCols = D / 4 / kStep;  // of a thread
+  const int c0 = blockIdx.y * (kMergeThreads / kTileRows) + threadIdx.x / kTileRows;
   // part 0 is CTA b's second slot, part k > 0 the first of CTA b + k
   const float *lse = a.part_lse + (size_t)(2 * b) * kTileRows + t;
+  const float4 *val = a.part_o + ((size_t)(2 * b) * (D / 4) + c0) * kTileRows + t;
   auto slot = [&](int k) { return 2 * k + (k == 0 ? 1 : 0); };
-  auto lse_of = [&](int k) {
-    return k < it.parts ? __ldcg(lse + slot(k) * kTileRows) : -INFINITY;
+  auto value = [&](int k, int c) {
+    return __ldcg(val + ((size_t)slot(k) * (D / 4) + c * kStep) * kTileRows);
   };
-  float M = -INFINITY, x[4];
-#pragma unroll 1
-  for (int k = (it.parts - 1) & ~3; k >= 0; k -= 4) {  // the first four last: they stay in x
+  const float x0 = __ldcg(lse + slot(0) * kTileRows);
+  float x1 = -INFINITY;
+  float4 v0[kCols], v1[kCols];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) x[u] = lse_of(k + u);
-    M = fmaxf(M, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+  for (int c = 0; c < kCols; ++c) v0[c] = value(0, c);
+  if (b + 1 < gridDim.x) {
+    x1 = __ldcg(lse + slot(1) * kTileRows);
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) v1[c] = value(1, c);
   }
+  const TreeJoin it = a.join[b];
+  if (it.parts == 0) return;
+  const int G = a.group, r = it.m * kTileRows + t;
+  if (r >= it.rows) return;
+  float M = fmaxf(x0, x1);
+#pragma unroll 4
+  for (int k = 2; k < it.parts; ++k) M = fmaxf(M, __ldcg(lse + slot(k) * kTileRows));
   const float ref = M == -INFINITY ? 0.f : M;
-  uint16_t *out = a.out + ((size_t)(it.q0 + r / G) * a.q_heads + it.g * G + r % G) * D;
-  constexpr int kStep = kMergeThreads / kTileRows;
-#pragma unroll 2
-  for (int c = blockIdx.y * kStep + threadIdx.x / kTileRows; c < D / 4; c += kMergeSplit * kStep) {
-    const float4 *src = a.part_o + ((size_t)(2 * b) * (D / 4) + c) * kTileRows + t;
-    float L = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-    for (int k = 0; k < it.parts; k += 4) {
-      float4 v[4];
-      float w[4];
+  float L = 0.f;
+  float4 o[kCols];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k + u < it.parts) v[u] = __ldcg(src + (size_t)slot(k + u) * (D / 4) * kTileRows);
-      }
+  for (int c = 0; c < kCols; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float w, const float4(&v)[kCols]) {
+    L += w;
+    if (w != 0.f)  // a part that saw nothing, or whose weight vanishes, adds nothing
 #pragma unroll
-      for (int u = 0; u < 4; ++u) w[u] = exp2f((k == 0 ? x[u] : lse_of(k + u)) - ref);
+      for (int c = 0; c < kCols; ++c)
+        o[c] = make_float4(fmaf(w, v[c].x, o[c].x), fmaf(w, v[c].y, o[c].y),
+                           fmaf(w, v[c].z, o[c].z), fmaf(w, v[c].w, o[c].w));
+  };
+  add(exp2f(x0 - ref), v0);
+  add(exp2f(x1 - ref), v1);
+#pragma unroll 4
+  for (int k = 2; k < it.parts; ++k) {
+    float4 v[kCols];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        L += w[u];
-        // a part that saw nothing, or whose weight vanishes, adds nothing
-        if (w[u] != 0.f)
-          o = make_float4(fmaf(w[u], v[u].x, o.x), fmaf(w[u], v[u].y, o.y),
-                          fmaf(w[u], v[u].z, o.z), fmaf(w[u], v[u].w, o.w));
-      }
-    }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    *reinterpret_cast<uint2 *>(out + 4 * c) =
-        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    for (int c = 0; c < kCols; ++c) v[c] = value(k, c);
+    add(exp2f(__ldcg(lse + slot(k) * kTileRows) - ref), v);
   }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  uint16_t *out = a.out + ((size_t)(it.q0 + r / G) * a.q_heads + it.g * G + r % G) * D + 4 * c0;
+#pragma unroll
+  for (int c = 0; c < kCols; ++c)
+    *reinterpret_cast<uint2 *>(out + 4 * kStep * c) =
+        make_uint2(pack_bf16(o[c].x * inv, o[c].y * inv), pack_bf16(o[c].z * inv, o[c].w * inv));
 }
 
 // Workspace: join records, then the parts' log-sum-exps and outputs.
