@@ -369,14 +369,15 @@ int paged_tree_masks(uint64_t *masks, int32_t *positions, const int32_t *parents
  *   t = positions[pair_axis[i]][t] * inv_freq[i]
  * with pairs (y[i], y[i + rotary_dim/2]), or (y[2i], y[2i+1]) with interleaved != 0;
  * elements at or past rotary_dim pass.  v is written as it is.  Computed in fp32 and rounded
- * once.  Angles are exact to about 2^-53 times the position (any int32 position).
+ * once.  Angles: a pair's turns per position are held to 64 bits after the point, so any int32
+ * position's are exact to 2^-33 of a turn beyond inv_freq's own rounding.
  * q, k, v, q_out: head rows of head_dim elements, heads adjacent, tokens *_stride elements
  * apart (multiples of 8, at least the row of heads), so they may be slices of one packed
  * projection.  q_out may be q itself (same address and stride); other overlap is not
  * allowed.  positions: int32, axis a of token t at a * axis_stride + t (axis_stride 0: all
  * axes share them).  num_axes 1..4.  pair_axis: HOST array of rotary_dim/2 bytes, read
  * during the call (NULL: axis 0; an entry >= num_axes returns PKV_ERR_ARG).  inv_freq: fp64
- * device array of rotary_dim/2 radians per position.  rotary_dim: 0 or a multiple of 16 up
+ * device array of rotary_dim/2 radians per position, finite and below 2^53.  rotary_dim: 0 or a multiple of 16 up
  * to head_dim; head_dim 64 or 128.  A negative slot writes no k and v (q_out is written); a
  * slot outside the pool sets PKV_DEV_BAD_SLOT and does the same.
  */
@@ -423,7 +424,7 @@ size_t paged_attention_tree_workspace_size(int num_q_heads, int num_kv_heads, in
  * over those t, as paged_attention_prefill computes it (scale > 0).  A row that sees no
  * token gives zeros.  A token that a row does not see takes no part in it, whatever its K
  * and V rows hold.  The drafts' K/V must be in the cache.  max_query_len: host bound of
- * every L, at most 64 mask_words.  A sequence with L > max_query_len, L > context_lens[s], a
+ * every L, at most 64 mask_words (0: nothing is queued).  A sequence with L > max_query_len, L > context_lens[s], a
  * context beyond its block table or rows outside [0, num_tokens] sets PKV_DEV_BAD_CONTEXT
  * and its rows are left unwritten; a bad block id sets PKV_DEV_BAD_BLOCK and the rows of its
  * sequence are unspecified.  L == 1 with bit 0 is a decode row.  The key range of one

@@ -527,7 +527,9 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
         const bool odd = bits >= 0x7f80;  // an infinity or NaN: no finite score in this row
         const int e = odd || bits == 0 ? 0 : min(134 - (bits >> 7), 120);
         const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-        sl *= __uint_as_float((uint32_t)(127 - e) << 23);
+        // not to zero, which times a masked score's -inf is NaN; the scores that 2^-126 stands
+        // in for are below 2^-100 either way
+        sl = fmaxf(sl * __uint_as_float((uint32_t)(127 - e) << 23), 1.17549435e-38f);
 #pragma unroll 1
         for (int c = 0; c < 2 * H; ++c) {  // 32 elements; the row moves down by as many
           uint32_t q1[8], q2[8];
@@ -905,27 +907,29 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
     bool more = advance();
     int aj = seg.j0, issued = 0, slot_in = 0;
     uint32_t empty_parity = 1;  // of the ring's previous round
-    // The table's entry of key tile j for this lane's block (INT_MIN: past the context).  Read
-    // one tile before it is looked at, so that nothing waits for the load.
-    auto block_of = [&](const Segment &g, int j) {
+    // The table's entry of key tile j for this lane's block (`held`: not past the context).
+    // Read one tile before it is looked at, so that nothing waits for the load.
+    bool held = false;
+    int next_blk = -1;
+    auto read_block = [&](int j) {
       const int tok = j * kTileKeys + lane * kBlockSize;
-      if (lane >= kTileBlocks || tok >= g.ctx) return INT_MIN;
-      return a.block_tables[(size_t)g.s * a.max_blocks + tok / kBlockSize];
+      held = lane < kTileBlocks && tok < seg.ctx;
+      if (held) next_blk = a.block_tables[(size_t)seg.s * a.max_blocks + tok / kBlockSize];
     };
-    int next_blk = more ? block_of(seg, aj) : INT_MIN;
+    if (more) read_block(aj);
     // Queues the run's next tile once its slot is free; false: gave up.
     auto issue = [&]() {
-      int blk = next_blk;
+      int blk = held ? next_blk : -1;
       const int g = seg.g;
-      if (blk != INT_MIN && (unsigned)blk >= (unsigned)a.num_blocks) {
+      if (held && (unsigned)blk >= (unsigned)a.num_blocks) {
         flag_error(a.err, PKV_DEV_BAD_BLOCK);
-        blk = INT_MIN;
+        blk = -1;
       }
       if (++aj >= seg.j1) {
         more = advance();
         aj = seg.j0;
       }
-      if (more) next_blk = block_of(seg, aj);  // one tile ahead
+      if (more) read_block(aj);  // one tile ahead
       if (issued >= slots && !mbar_wait(empty + 8 * slot_in, empty_parity, abort_flag, a.err))
         return false;
       if (lane < kTileBlocks) {
@@ -1221,7 +1225,8 @@ extern "C" {
 size_t paged_attention_tree_workspace_size(int num_q_heads, int num_kv_heads, int head_dim,
                                            int max_query_len) {
   if (num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
-      head_dim <= 0 || max_query_len < 0)
+      (head_dim != 64 && head_dim != 128) || max_query_len < 0 ||
+      max_query_len > PKV_TREE_MAX_TOKENS)
     return 0;
   return tree_workspace(num_q_heads / num_kv_heads, head_dim, max_query_len).total;
 }

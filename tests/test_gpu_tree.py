@@ -425,6 +425,50 @@ def test_attention_flags(ops):
     assert_within(out[30:], ref[30:], bound[30:])
 
 
+@pytest.mark.parametrize("bad", [-1, -2**31, 2**31 - 1])
+@pytest.mark.parametrize("f8", [False, True])
+def test_attention_bad_block_ids(ops, f8, bad):
+    w = Tree([(50, 10), (60, 20), (70, 5)], 4, 2, 128, seed=16, f8=f8)
+    ref, bound = w.attention64()
+    w.bt[1, 1] = bad
+    out, d = run_tree(ops, w)
+    assert int(d["err"]) == ops.DEV_BAD_BLOCK
+    assert_within(out[:10], ref[:10], bound[:10])
+    assert_within(out[30:], ref[30:], bound[30:])
+
+
+@pytest.mark.parametrize("q_size,k_scale", [(1e-20, 1e-30), (1e-38, 1e-8), (1.0, 1e-44)])
+def test_e4m3_scores_that_vanish(ops, q_size, k_scale):
+    """Scores below fp32's range weigh every visible token alike, and masked ones not at all."""
+    w = Tree([(70, 40), (30, 30), (700, 9)], 8, 2, 128, seed=17, f8=True)
+    w.q = (w.q.float() * q_size).to(torch.bfloat16)
+    w.ks.fill_(k_scale)
+    out, d = run_tree(ops, w)
+    ref, bound = w.attention64()
+    assert_within(out, ref, bound)
+    assert int(d["err"]) == 0
+
+
+@pytest.mark.parametrize("f8", [False, True])
+def test_two_calls_at_once(ops, f8):
+    """Calls on two streams, each with its own workspace and inputs, interleaved."""
+    ws = [Tree([(900, 30), (1500, 20)], 8, 2, 128, seed=18, f8=f8),
+          Tree([(64, 64), (2000, 3), (17, 2)], 8, 4, 64, seed=19, f8=f8)]
+    ds = [w.cuda() for w in ws]
+    streams = [torch.cuda.Stream() for _ in ws]
+    outs = [torch.empty(w.T, w.Hq, w.D, dtype=torch.bfloat16, device="cuda") for w in ws]
+    scratch = [ops.alloc_tree_workspace(w.Hq, w.Hkv, w.D, w.maxq) for w in ws]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for w, d, st, o, sc in zip(ws, ds, streams, outs, scratch):
+            run_tree(ops, w, d=d, ws=sc, out=o, stream=st)
+    torch.cuda.synchronize()
+    for w, d, o in zip(ws, ds, outs):
+        ref, bound = w.attention64()
+        assert_within(o, ref, bound)
+        assert int(d["err"]) == 0
+
+
 def test_cache_offsets_past_32_bits(ops):
     """Blocks at the far end of a cache of more than 2^31 elements."""
     w = Tree([(200, 20), (90, 7)], 8, 8, 128, seed=15, poison=False)

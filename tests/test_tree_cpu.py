@@ -97,6 +97,13 @@ def test_attention_refusals(fp8):
     assert lib().paged_attention_tree_workspace_size(8, 2, 128, -1) == 0
 
 
+def test_workspace_of_sizes_out_of_range():
+    """No size for what the call itself refuses."""
+    f = lib().paged_attention_tree_workspace_size
+    for k in ((8, 2, 96, 8), (8, 2, 128, 1025), (0, 1, 64, 8), (8, 0, 64, 8)):
+        assert f(*k) == 0, k
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_commit_refusals(fp8):
     f = lib().paged_tree_commit_fp8 if fp8 else lib().paged_tree_commit
