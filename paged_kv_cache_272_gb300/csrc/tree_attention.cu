@@ -28,8 +28,10 @@
 // results (at most two per CTA, so the workspace does not grow with the batch) that
 // tree_merge_kernel joins by their log-sum-exp in the order of the keys; nothing is summed
 // in an order that depends on timing.  Each CTA finds its run from context_lens by itself:
-// one launch for the attention, one for the join.  Row tiles of one pair are run in step by
-// neighbouring CTAs, so that the cache is read from DRAM once and from L2 for the others.
+// one launch for the attention, one for the join.  The row tiles of a pair are run by
+// neighbouring CTAs, which start together and stay near enough for the cache to come from DRAM
+// once and from L2 for the others (eight sequences of 65536 tokens, three row tiles: 703 us;
+// 776 with one row tile's CTAs after the other's, which drift apart by more than L2 holds).
 //
 // Masked values.  A weight of zero times a V element that is not finite would spoil a row
 // that does not see it.  Tiles that overlap the tree (every row sees the others) are checked:
@@ -57,10 +59,10 @@ constexpr int kTileKeys = 64;
 constexpr int kTileBlocks = kTileKeys / kBlockSize;
 // Threads per CTA: warps 0-3 softmax, 4-7 products and copies, 8-11 (E4M3) widening.
 __host__ __device__ constexpr int tree_threads(bool f8) { return f8 ? 384 : 256; }
-// E4M3: 384 threads of 80 registers, twice per SM; the softmax warps take 144 and the others
-// leave 48 (128 x 144 + 256 x 48 = 384 x 80).  Batch of 64: 185 us with 112 / 64, 180 with
-// 128 / 56, 173 with 144 / 48.
-constexpr int kLaunchRegs = 80, kSoftmaxRegs = 144, kOtherRegs = 48;
+// E4M3: 384 threads of 80 registers, twice per SM; the softmax warps take 160 and the others
+// leave 40 (128 x 160 + 256 x 40 = 384 x 80).  Batch of 64: 182 us with 128 / 56, 173 with
+// 144 / 48, 169 with 160 / 40.
+constexpr int kLaunchRegs = 80, kSoftmaxRegs = 160, kOtherRegs = 40;
 static_assert(128 * kSoftmaxRegs + 256 * kOtherRegs <= 384 * kLaunchRegs, "register split");
 constexpr uint32_t kTmemColumns = 256;
 constexpr int kMaxRowTiles = 64;  // row tiles of one launch
@@ -127,20 +129,69 @@ __device__ __forceinline__ SeqInfo seq_info(const TreeArgs &a, int s, bool flag)
 // any segment takes to start and finish (Q, first scores, last product, output).  A run that
 // meets many short pairs so gets fewer tiles.
 struct Plan {
-  unsigned long long tiles[kMaxRowTiles];  // units of row tile m (all KV heads); later the
-                                           // ring of segments
+  unsigned long long tiles[kMaxRowTiles];  // units of row tile m (all KV heads), its CTAs in
+                                           // the top 16 bits (2^48 units are years of work);
+                                           // later the ring of segments
   unsigned long long warp_sum[tree_threads(true) / 32];
   unsigned long long off;  // first unit within sequence s (KV heads end to end)
   long long left;          // units of the run
   long long cta_tiles, extra;  // run length of this row tile's CTAs: cta_tiles, one more for
-  int ctas, cta;               // the first `extra` of its `ctas`; this CTA's number there
-  int s, m;
+  int cta, slot;               // the first `extra`; this CTA's number there, and its place in
+  int s, m;                    // the workspace (the numbers of all row tiles end to end)
 };
 
 // floor(a b / c), b <= c, without a 128-bit product: b and c lose low bits they do not need.
 __device__ __forceinline__ int share(int a, unsigned long long b, unsigned long long c) {
   while (c >> 48) b >>= 1, c >>= 1;
   return (int)((unsigned long long)a * b / c);
+}
+
+// CTAs for that many units.
+__device__ __forceinline__ int most_ctas(unsigned long long units, int ctas) {
+  const unsigned long long few = (units + kMinRun - 1) / kMinRun;
+  return few < (unsigned long long)ctas ? (int)few : ctas;
+}
+
+// Several row tiles, one thread: this CTA's row tile (p->m), its number c there, its place in
+// the workspace, the row tile's CTAs n and units.  Not inlined: inlined, it took registers from
+// the loops (E4M3 batch 176 -> 200 us).
+struct RowTileShare {
+  unsigned long long units;
+  int c, n, m, slot;
+};
+__device__ __noinline__ RowTileShare row_tile_share(unsigned long long *tiles, int row_tiles,
+                                                     int kv_heads, int runs) {
+  RowTileShare o = {0, (int)blockIdx.x, 0, 0, (int)blockIdx.x};
+  unsigned long long total = 0;
+#pragma unroll 1
+  for (int m = row_tiles - 1; m >= 0; --m) {
+    o.units += tiles[m] * (unsigned)kv_heads;
+    tiles[m] = o.units;
+    total += o.units;
+  }
+  int k = 0;
+#pragma unroll 1
+  for (; k < row_tiles && tiles[k]; ++k)
+    tiles[k] |= (unsigned long long)most_ctas(tiles[k], max(share(runs, tiles[k], total), 1)) << 48;
+  // The row tiles' CTAs of one number are neighbours (a row tile has no more than the one
+  // before it): while k row tiles have CTAs left, k at a time.
+  int from = 0;
+#pragma unroll 1
+  for (; k > 0; --k) {
+    const int upto = (int)(tiles[k - 1] >> 48), level = (upto - from) * k;
+    if (o.c < level) {
+      o.m = o.c % k, o.c = from + o.c / k;
+      o.units = tiles[o.m] & ((1ull << 48) - 1);
+      o.n = (int)(tiles[o.m] >> 48);
+      o.slot = o.c;
+#pragma unroll 1
+      for (int i = 0; i < o.m; ++i) o.slot += (int)(tiles[i] >> 48);
+      break;
+    }
+    o.c -= level;
+    from = upto;
+  }
+  return o;
 }
 
 // Which key tiles this CTA runs (all threads; the result in *p after the last barrier).  Short
@@ -168,43 +219,28 @@ __device__ __forceinline__ void plan_run(const TreeArgs &a, Plan *p) {
   }
   __syncthreads();
   if (tid == 0) {
-    unsigned long long sum = 0, total = 0;
+    RowTileShare o = {0, (int)blockIdx.x, 0, 0, (int)blockIdx.x};
     if (one) {
 #pragma unroll 1
-      for (int w = 0; w < kThreads / 32; ++w) sum += p->warp_sum[w];
-      p->tiles[0] = total = sum * (unsigned)a.kv_heads;
+      for (int w = 0; w < kThreads / 32; ++w) o.units += p->warp_sum[w];
+      o.units *= (unsigned)a.kv_heads;
+      o.n = most_ctas(o.units, a.runs);
     } else {
-#pragma unroll 1
-      for (int m = a.row_tiles - 1; m >= 0; --m) {
-        sum += p->tiles[m] * (unsigned)a.kv_heads;
-        p->tiles[m] = sum;
-        total += sum;
-      }
+      o = row_tile_share(p->tiles, a.row_tiles, a.kv_heads, a.runs);
     }
-    int at = 0;
-#pragma unroll 1
-    for (int m = 0; m < a.row_tiles && p->tiles[m]; ++m) {
-      const unsigned long long w = p->tiles[m];
-      int n = one ? a.runs : share(a.runs, w, total);
-      if ((unsigned long long)n > (w + kMinRun - 1) / kMinRun) n = (int)((w + kMinRun - 1) / kMinRun);
-      if (n < 1) n = 1;
-      const int c = (int)blockIdx.x - at;
-      if (c < n) {
-        unsigned long long q, r;
-        if (w >> 32)
-          q = w / (unsigned)n, r = w % (unsigned)n;
-        else
-          q = (unsigned)w / (unsigned)n, r = (unsigned)w % (unsigned)n;
-        p->m = a.m0 + m;
-        p->ctas = n;
-        p->cta = c;
-        p->cta_tiles = (long long)q;
-        p->extra = (long long)r;
-        p->left = (long long)q + (c < (long long)r ? 1 : 0);
-        p->off = (unsigned)c * q + min((long long)c, (long long)r);
-        break;
-      }
-      at += n;
+    p->slot = o.slot;  // its own even with nothing to do
+    if (o.c < o.n) {
+      unsigned long long q, r;
+      if (o.units >> 32)
+        q = o.units / (unsigned)o.n, r = o.units % (unsigned)o.n;
+      else
+        q = (unsigned)o.units / (unsigned)o.n, r = (unsigned)o.units % (unsigned)o.n;
+      p->m = a.m0 + o.m;
+      p->cta = o.c;
+      p->cta_tiles = (long long)q;
+      p->extra = (long long)r;
+      p->left = (long long)q + (o.c < (long long)r ? 1 : 0);
+      p->off = (unsigned)o.c * q + min((long long)o.c, (long long)r);
     }
   }
   __syncthreads();
@@ -257,13 +293,14 @@ struct __align__(16) Segment {
 constexpr int kSegRing = 8;
 static_assert(kSegRing * sizeof(Segment) <= kMaxRowTiles * sizeof(unsigned long long), "ring");
 
+// Lives in shared memory (one lane of the K warp moves it on): the copying warps have few
+// registers to spare.
 struct Walk {
-  const TreeArgs &a;
   long long left;
-  int m, s, g, unit;
+  int s, g, unit;
   SeqInfo i;
-  __device__ Walk(const TreeArgs &args, const Plan &p)
-      : a(args), left(p.left), m(p.m), s(p.s), g(0), unit(0) {
+  __device__ __forceinline__ void begin(const TreeArgs &a, const Plan &p) {
+    left = p.left, s = p.s;
     i = seq_info(a, s, false);
     const unsigned n = (unsigned)(i.tiles + a.start);
     if (p.off >> 32) {
@@ -272,14 +309,15 @@ struct Walk {
       g = (int)((unsigned)p.off / n), unit = (int)((unsigned)p.off % n);
     }
   }
-  __device__ bool next(Segment &o) {
+  __device__ __forceinline__ void next(const TreeArgs &a, int m, Segment &o) {
     while (left > 0) {
       if (g == a.kv_heads) {
         g = 0;
         do {
-          if (++s >= a.num_seqs) return false;  // not reached: the run's units are counted
-          i = seq_info(a, s, false);
-        } while (i.tiles == 0 || i.row_tiles <= m);
+          if (++s >= a.num_seqs) left = 0;  // not reached: the run's units are counted
+          else i = seq_info(a, s, false);
+        } while (left > 0 && (i.tiles == 0 || i.row_tiles <= m));
+        if (left == 0) break;
       }
       const int end = (int)min((long long)(i.tiles + a.start), unit + left);
       left -= end - unit;
@@ -287,11 +325,12 @@ struct Walk {
       o.j0 = max(unit - a.start, 0), o.j1 = max(end - a.start, 0);
       unit = 0;
       ++g;
-      if (o.j1 > o.j0) return true;
+      if (o.j1 > o.j0) return;
     }
-    return false;
+    o.j0 = o.j1 = 0;
   }
 };
+static_assert(sizeof(Walk) <= sizeof(Plan::warp_sum), "the plan's sums make room for it");
 
 // Shared memory of one CTA (two per SM).  D: head dim; F8: E4M3 cache.
 template <int D, bool F8>
@@ -452,16 +491,18 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
   pdl_wait();
   plan_run<tree_threads(F8)>(a, plan);
   if (plan->left == 0) {
-    if (threadIdx.x == 0) a.join[blockIdx.x].parts = 0;
+    if (threadIdx.x == 0) a.join[plan->slot].parts = 0;
     return;
   }
   if (warp == 4) alloc(smem_u32(tmem_slot), kTmemColumns);
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const uint32_t tS = tmem, tP = tmem + 64, tQ = tmem + 96, tO = tmem + 128;
-  const int G = a.group, r0 = plan->m * kTileRows;
+  const int G = a.group;
+  // Columns of TMEM: S, P, the part of Q kept there, O.  A role reads what it needs of these for
+  // itself; held across the split into roles, they were spilled in all of them.
+  const volatile uint32_t *tmem_at = tmem_slot;
+  const volatile int *row_tile = &plan->m;
   Segment *ring_seg = reinterpret_cast<Segment *>(plan->tiles);
   Segment seg;
   // The run's segment n; false: the run is over (or a wait gave up).
@@ -475,13 +516,16 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
   if (warp < 4) {
     if constexpr (F8) set_regs_up<kSoftmaxRegs>();
     // ---------------- softmax warps: thread t owns row t ----------------
+    const uint32_t tmem = *tmem_at;
+    const uint32_t tS = tmem, tP = tmem + 64, tQ = tmem + 96, tO = tmem + 128;
+    const int r0 = *row_tile * kTileRows;
     const int t = threadIdx.x;
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
     const int r = r0 + t;
     int jt = 0;   // tiles done (the barriers' phases)
     int nseg = 0; // segments begun
     bool ok = true;
-    if (t == 0) a.join[blockIdx.x].parts = 0;
+    if (t == 0) a.join[plan->slot].parts = 0;
     while (ok && segment(nseg)) {
       ++nseg;
       const int rows = seg.L * G;
@@ -717,7 +761,7 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
           if (v_bad[j - tree_tile] == nseg) bad |= 1u << (j - tree_tile);
       const bool whole = seg.j0 == 0 && seg.j1 == seg.tiles;
       const float inv = l == 0.f ? 0.f : vs / l;
-      const size_t part = ((size_t)blockIdx.x * 2 + (seg.j0 > 0 ? 0 : 1)) * kTileRows + t;
+      const size_t part = ((size_t)plan->slot * 2 + (seg.j0 > 0 ? 0 : 1)) * kTileRows + t;
       if (whole) {
         // through this warp's rows of the staging region, so that a row's 128 bytes leave by
         // adjacent lanes
@@ -777,7 +821,7 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
         int parts = 1;
         for (long long rest = seg.tiles - seg.j1; rest > 0; ++parts)
           rest -= plan->cta_tiles + (plan->cta + parts < plan->extra ? 1 : 0);
-        a.join[blockIdx.x] = TreeJoin{seg.q0, rows, seg.g, plan->m, parts, {0, 0, 0}};
+        a.join[plan->slot] = TreeJoin{seg.q0, rows, seg.g, plan->m, parts, {0, 0, 0}};
       }
     }
     fence_before();
@@ -785,6 +829,7 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
   if constexpr (F8) set_regs_down<kOtherRegs>();
   if (warp == 4) {
     // ---------------- S warp: lane 0 issues S = Q K^T ----------------
+    const uint32_t tmem = *tmem_at, tS = tmem, tQ = tmem + 96;
     constexpr uint32_t id = F8 ? idesc_e4m3(kTileRows, kTileKeys) : idesc(kTileRows, kTileKeys, false, false);
     int jt = 0, ok = 1;
     for (int nseg = 0; ok && segment(nseg); ++nseg) {
@@ -836,6 +881,7 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
     fence_before();
   } else if (warp == 7) {
     // ---------------- P V warp: lane 0 issues O += P V ----------------
+    const uint32_t tmem = *tmem_at, tP = tmem + 64, tO = tmem + 128;
     fence_after();
     // bf16: V [keys][D] (MN-major); E4M3: V widened to [D][keys] (K-major)
     constexpr uint32_t id = idesc(kTileRows, D, F8, !F8);
@@ -870,6 +916,7 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
   } else if (warp < 7) {
     // ---------------- copying warps: warp 5 K, warp 6 V ----------------
     const bool is_v = warp == 6;
+    const int r0 = *row_tile * kTileRows;
     // one row tile: the cache is read once, its L2 lines go first; several: the row tiles of
     // a pair share them
     uint64_t pol;
@@ -882,19 +929,19 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
     const uint32_t full = F8 && is_v ? raw_full : is_v ? v_full : k_full;
     const uint32_t empty = F8 && is_v ? raw_empty : is_v ? v_empty : k_empty;
     const uint32_t ring = F8 && is_v ? base + Lay::kRawV : is_v ? sV : sK;
-    Walk walk(a, *plan);  // K warp
     int nseg = 0;
+    Walk *walk = reinterpret_cast<Walk *>(plan->warp_sum);
+    if (warp == 5 && lane == 0) walk->begin(a, *plan);
     // The next segment: the K warp finds and publishes it and asks for its Q rows, the V warp
     // takes it from the ring.
     auto advance = [&]() {
-      if (is_v) return segment(nseg++);
-      if (!walk.next(seg)) seg.j0 = seg.j1 = 0;
-      if (lane == 0) {
-        ring_seg[nseg % kSegRing] = seg;
+      if (!is_v && lane == 0) {
+        walk->next(a, plan->m, ring_seg[nseg % kSegRing]);
         mbar_arrive(seg_full + 8 * (nseg % kSegRing));
       }
-      ++nseg;
-      if (seg.j0 == seg.j1) return false;
+      __syncwarp();
+      if (!__all_sync(kFullMask, segment(nseg++))) return false;
+      if (is_v) return true;
 #pragma unroll 1
       for (int r = r0 + lane; r < min(r0 + kTileRows, seg.L * G); r += 32) {
         const uint16_t *p = a.q + ((size_t)(seg.q0 + r / G) * a.q_heads + seg.g * G + r % G) * D;
@@ -1034,7 +1081,7 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
   __syncthreads();
   if (warp == 4) {
     fence_after();
-    dealloc(tmem, kTmemColumns);
+    dealloc(*tmem_slot, kTmemColumns);
   }
 }
 
