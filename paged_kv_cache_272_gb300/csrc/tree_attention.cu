@@ -66,12 +66,13 @@ constexpr int kLaunchRegs = 80, kSoftmaxRegs = 160, kOtherRegs = 40;
 static_assert(128 * kSoftmaxRegs + 256 * kOtherRegs <= 384 * kLaunchRegs, "register split");
 constexpr uint32_t kTmemColumns = 256;
 constexpr int kMaxRowTiles = 64;  // row tiles of one launch
-// A segment's start and finish, in key tiles.  Measured, none / 4 / 8 / 12: 32 ragged sequences
-// 79.1 / 77.4 / 77.0 / 78.3 us, short MHA contexts 29.4 / 27.8 / 29.2 / 29.3; E4M3, 64 ragged
-// sequences 186 / 180 / 176 / 176 (q's two terms take longer to make).
-constexpr int kStart = 5, kStartF8 = 8;
-// Least units of a run: one sequence of 700 tokens takes 20.1 us with runs of one unit, 17.0
-// with 2, 15.2 with 4 (fewer parts to join), 16.5 with 6.
+// A segment's start and finish, in key tiles.  Measured, 3 / 4 / 5 / 6: 32 ragged sequences 77.9 /
+// 77.1 / 77.2 / 76.5 us, short MHA contexts 24.2 / 24.2 / 23.8 / 24.8; E4M3, 64 ragged
+// sequences, 6 / 8 / 10 / 12: 170 / 169 / 169 / 167 (q's two terms take longer to make).  None
+// at all: 79, 29, 186 (before other changes).
+constexpr int kStart = 5, kStartF8 = 12;
+// Least units of a run: one sequence of 700 tokens takes 14.6 us with runs of 3, 14.0 with 4
+// (fewer parts to join), 14.5 with 5, 15.2 with 6.
 constexpr int kMinRun = 4;
 
 struct TreeArgs {
@@ -131,14 +132,69 @@ __device__ __forceinline__ SeqInfo seq_info(const TreeArgs &a, int s, bool flag)
 struct Plan {
   unsigned long long tiles[kMaxRowTiles];  // units of row tile m (all KV heads), its CTAs in
                                            // the top 16 bits (2^48 units are years of work);
-                                           // later the ring of segments
+                                           // later the ring of segments and the walk
   unsigned long long warp_sum[tree_threads(true) / 32];
-  unsigned long long off;  // first unit within sequence s (KV heads end to end)
+  unsigned long long first;  // unit of the row tile
   long long left;          // units of the run
   long long cta_tiles, extra;  // run length of this row tile's CTAs: cta_tiles, one more for
   int cta, slot;               // the first `extra`; this CTA's number there, and its place in
-  int s, m;                    // the workspace (the numbers of all row tiles end to end)
+  int m;                       // the workspace (the numbers of all row tiles end to end)
 };
+
+// The segments of a run.  The K warp walks them in order, ahead of everyone, and hands them on
+// through a small ring in shared memory; one with no tiles ends the run.  It is at most eight
+// segments ahead of the slowest reader: K of tile t is copied once S of tile t - KS is done,
+// which the softmax warps' work on tile t - KS - 1 precedes, and the ring is written one tile
+// before that copy.
+struct __align__(16) Segment {
+  int s, g, q0, L, ctx, tiles, j0, j1;
+};
+constexpr int kSegRing = 8;
+static_assert(kSegRing * sizeof(Segment) <= kMaxRowTiles * sizeof(unsigned long long), "ring");
+
+// Where a run stands.  In shared memory (one lane of the K warp moves it on): the copying warps
+// have few registers to spare.
+struct Walk {
+  long long left;  // units
+  int s, g, unit;  // sequence, KV head, unit of the pair
+  SeqInfo i;
+  // The run's first unit is unit `off` of sequence s (KV heads end to end).
+  __device__ __forceinline__ void begin(const TreeArgs &a, int seq, const SeqInfo &info,
+                                        unsigned long long off, long long units) {
+    const unsigned n = (unsigned)(info.tiles + a.start);
+    left = units, s = seq, i = info;
+    if (off >> 32) {
+      g = (int)(off / n), unit = (int)(off % n);
+    } else {
+      g = (int)((unsigned)off / n), unit = (int)((unsigned)off % n);
+    }
+  }
+  __device__ __forceinline__ void next(const TreeArgs &a, int m, Segment &o) {
+    while (left > 0) {
+      if (g == a.kv_heads) {
+        g = 0;
+        do {
+          if (++s >= a.num_seqs) left = 0;  // not reached: the run's units are counted
+          else i = seq_info(a, s, false);
+        } while (left > 0 && (i.tiles == 0 || i.row_tiles <= m));
+        if (left == 0) break;
+      }
+      const int end = (int)min((long long)(i.tiles + a.start), unit + left);
+      left -= end - unit;
+      o.s = s, o.g = g, o.q0 = i.q0, o.L = i.L, o.ctx = i.ctx, o.tiles = i.tiles;
+      o.j0 = max(unit - a.start, 0), o.j1 = max(end - a.start, 0);
+      unit = 0;
+      ++g;
+      if (o.j1 > o.j0) return;
+    }
+    o.j0 = o.j1 = 0;
+  }
+};
+constexpr int kWalkAt = kSegRing * (int)sizeof(Segment);  // bytes into Plan::tiles
+static_assert(kWalkAt + sizeof(Walk) <= sizeof(Plan::tiles), "room behind the ring");
+__device__ __forceinline__ Walk *walk_of(Plan *p) {
+  return reinterpret_cast<Walk *>(reinterpret_cast<char *>(p->tiles) + kWalkAt);
+}
 
 // floor(a b / c), b <= c, without a 128-bit product: b and c lose low bits they do not need.
 __device__ __forceinline__ int share(int a, unsigned long long b, unsigned long long c) {
@@ -194,68 +250,79 @@ __device__ __noinline__ RowTileShare row_tile_share(unsigned long long *tiles, i
   return o;
 }
 
-// Which key tiles this CTA runs (all threads; the result in *p after the last barrier).  Short
-// on purpose: code that runs once is bound by the instruction fetch, ~20 cycles each.
+// One thread: run c of the n that share `units`.
+__device__ __forceinline__ void cut_run(Plan *p, unsigned long long units, int n, int c, int m,
+                                        int slot) {
+  p->slot = slot;  // its own even with nothing to do
+  p->left = 0;
+  if (c >= n) return;
+  unsigned long long q, r;
+  if (units >> 32)
+    q = units / (unsigned)n, r = units % (unsigned)n;
+  else
+    q = (unsigned)units / (unsigned)n, r = (unsigned)units % (unsigned)n;
+  p->m = m;
+  p->cta = c;
+  p->cta_tiles = (long long)q;
+  p->extra = (long long)r;
+  p->left = (long long)q + (c < (long long)r ? 1 : 0);
+  p->first = (unsigned)c * q + min((long long)c, (long long)r);
+}
+
+// Which key tiles this CTA runs (all threads; the result in *p and its walk after the last
+// barrier).  Short on purpose: code that runs once is bound by the instruction fetch, ~20 cycles
+// each.
 template <int kThreads>
 __device__ __forceinline__ void plan_run(const TreeArgs &a, Plan *p) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool one = a.row_tiles == 1;
-  if (!one && tid < kMaxRowTiles) p->tiles[tid] = 0;
-  if (tid == 0) p->left = 0;
-  if (!one) __syncthreads();
-  unsigned long long mine = 0;
+  // One row tile and a thread for every sequence: the units of a KV head are summed once, and
+  // the thread whose sequence the run begins in has what it needs.
+  const bool once = one && a.num_seqs <= kThreads;
+  SeqInfo i;
+  i.tiles = 0;
+  if (!once) {
+    if (!one && tid < kMaxRowTiles) p->tiles[tid] = 0;
+    if (!one) __syncthreads();
+    unsigned long long mine = 0;
 #pragma unroll 1
-  for (int s = tid; s < a.num_seqs; s += kThreads) {
-    const SeqInfo i = seq_info(a, s, blockIdx.x == 0);
-    const int last = min(i.row_tiles - a.m0, a.row_tiles);
-    if (i.tiles == 0 || last <= 0) continue;
-    mine += i.tiles + a.start;
-    if (!one) atomicAdd(&p->tiles[last - 1], (unsigned long long)(i.tiles + a.start));
-  }
-  if (one) {
-#pragma unroll 1
-    for (int off = 16; off > 0; off >>= 1) mine += __shfl_xor_sync(kFullMask, mine, off);
-    if (lane == 0) p->warp_sum[warp] = mine;
-  }
-  __syncthreads();
-  if (tid == 0) {
-    RowTileShare o = {0, (int)blockIdx.x, 0, 0, (int)blockIdx.x};
+    for (int s = tid; s < a.num_seqs; s += kThreads) {
+      i = seq_info(a, s, blockIdx.x == 0);
+      const int last = min(i.row_tiles - a.m0, a.row_tiles);
+      if (i.tiles == 0 || last <= 0) continue;
+      mine += i.tiles + a.start;
+      if (!one) atomicAdd(&p->tiles[last - 1], (unsigned long long)(i.tiles + a.start));
+    }
     if (one) {
 #pragma unroll 1
-      for (int w = 0; w < kThreads / 32; ++w) o.units += p->warp_sum[w];
-      o.units *= (unsigned)a.kv_heads;
-      o.n = most_ctas(o.units, a.runs);
-    } else {
-      o = row_tile_share(p->tiles, a.row_tiles, a.kv_heads, a.runs);
+      for (int off = 16; off > 0; off >>= 1) mine += __shfl_xor_sync(kFullMask, mine, off);
+      if (lane == 0) p->warp_sum[warp] = mine;
     }
-    p->slot = o.slot;  // its own even with nothing to do
-    if (o.c < o.n) {
-      unsigned long long q, r;
-      if (o.units >> 32)
-        q = o.units / (unsigned)o.n, r = o.units % (unsigned)o.n;
-      else
-        q = (unsigned)o.units / (unsigned)o.n, r = (unsigned)o.units % (unsigned)o.n;
-      p->m = a.m0 + o.m;
-      p->cta = o.c;
-      p->cta_tiles = (long long)q;
-      p->extra = (long long)r;
-      p->left = (long long)q + (o.c < (long long)r ? 1 : 0);
-      p->off = (unsigned)o.c * q + min((long long)o.c, (long long)r);
+    __syncthreads();
+    if (tid == 0) {
+      RowTileShare o = {0, (int)blockIdx.x, 0, 0, (int)blockIdx.x};
+      if (one) {
+#pragma unroll 1
+        for (int w = 0; w < kThreads / 32; ++w) o.units += p->warp_sum[w];
+        o.units *= (unsigned)a.kv_heads;
+        o.n = most_ctas(o.units, a.runs);
+      } else {
+        o = row_tile_share(p->tiles, a.row_tiles, a.kv_heads, a.runs);
+      }
+      cut_run(p, o.units, o.n, o.c, a.m0 + o.m, o.slot);
     }
+    __syncthreads();
+    if (p->left == 0) return;
   }
-  __syncthreads();
-  if (p->left == 0) return;
-  const unsigned long long u0 = p->off;
-  const int m = p->m;
+  const int m = once ? a.m0 : p->m;
   unsigned long long base = 0;
 #pragma unroll 1
   for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) {
     const int s = s0 + tid;
     unsigned long long n = 0;
     if (s < a.num_seqs) {
-      const SeqInfo i = seq_info(a, s, false);
-      if (i.tiles > 0 && i.row_tiles > m)
-        n = (unsigned long long)(i.tiles + a.start) * a.kv_heads;
+      i = seq_info(a, s, once && blockIdx.x == 0);
+      if (i.tiles > 0 && i.row_tiles > m) n = (unsigned long long)(i.tiles + a.start);
     }
     unsigned long long incl = n;
 #pragma unroll 1
@@ -267,70 +334,27 @@ __device__ __forceinline__ void plan_run(const TreeArgs &a, Plan *p) {
     __syncthreads();
     unsigned long long first = base + incl - n;
 #pragma unroll 1
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < kThreads / 32 && s0 + 32 * w < a.num_seqs; ++w) {
       const unsigned long long v = p->warp_sum[w];
       if (w < warp) first += v;
       base += v;
     }
-    if (n && u0 >= first && u0 < first + n) {
-      p->s = s;
-      p->off = u0 - first;
+    if (once) {
+      if (tid == 0) {
+        const unsigned long long units = base * (unsigned)a.kv_heads;
+        cut_run(p, units, most_ctas(units, a.runs), blockIdx.x, m, blockIdx.x);
+      }
+      __syncthreads();
     }
-    if (u0 < base) break;
+    first *= (unsigned)a.kv_heads;
+    const unsigned long long u0 = p->first;
+    if (p->left && u0 >= first && u0 - first < n * (unsigned)a.kv_heads)
+      walk_of(p)->begin(a, s, i, u0 - first, p->left);
+    if (once || u0 < base * (unsigned)a.kv_heads) break;
     __syncthreads();
   }
   __syncthreads();
 }
-
-// The segments of a run.  The K warp walks them in order, ahead of everyone, and hands them on
-// through a small ring in shared memory; one with no tiles ends the run.  It is at most eight
-// segments ahead of the slowest reader: K of tile t is copied once S of tile t - KS is done,
-// which the softmax warps' work on tile t - KS - 1 precedes, and the ring is written one tile
-// before that copy.
-struct __align__(16) Segment {
-  int s, g, q0, L, ctx, tiles, j0, j1;
-};
-constexpr int kSegRing = 8;
-static_assert(kSegRing * sizeof(Segment) <= kMaxRowTiles * sizeof(unsigned long long), "ring");
-
-// Lives in shared memory (one lane of the K warp moves it on): the copying warps have few
-// registers to spare.
-struct Walk {
-  long long left;
-  int s, g, unit;
-  SeqInfo i;
-  __device__ __forceinline__ void begin(const TreeArgs &a, const Plan &p) {
-    left = p.left, s = p.s;
-    i = seq_info(a, s, false);
-    const unsigned n = (unsigned)(i.tiles + a.start);
-    if (p.off >> 32) {
-      g = (int)(p.off / n), unit = (int)(p.off % n);
-    } else {
-      g = (int)((unsigned)p.off / n), unit = (int)((unsigned)p.off % n);
-    }
-  }
-  __device__ __forceinline__ void next(const TreeArgs &a, int m, Segment &o) {
-    while (left > 0) {
-      if (g == a.kv_heads) {
-        g = 0;
-        do {
-          if (++s >= a.num_seqs) left = 0;  // not reached: the run's units are counted
-          else i = seq_info(a, s, false);
-        } while (left > 0 && (i.tiles == 0 || i.row_tiles <= m));
-        if (left == 0) break;
-      }
-      const int end = (int)min((long long)(i.tiles + a.start), unit + left);
-      left -= end - unit;
-      o.s = s, o.g = g, o.q0 = i.q0, o.L = i.L, o.ctx = i.ctx, o.tiles = i.tiles;
-      o.j0 = max(unit - a.start, 0), o.j1 = max(end - a.start, 0);
-      unit = 0;
-      ++g;
-      if (o.j1 > o.j0) return;
-    }
-    o.j0 = o.j1 = 0;
-  }
-};
-static_assert(sizeof(Walk) <= sizeof(Plan::warp_sum), "the plan's sums make room for it");
 
 // Shared memory of one CTA (two per SM).  D: head dim; F8: E4M3 cache.
 template <int D, bool F8>
@@ -489,15 +513,18 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
   }
   pdl_trigger();
   pdl_wait();
+  // After the wait: a kernel before this one may still have to allocate its own.
+  if (warp == 4) {
+    alloc(smem_u32(tmem_slot), kTmemColumns);
+    fence_before();
+  }
   plan_run<tree_threads(F8)>(a, plan);
+  fence_after();
   if (plan->left == 0) {
     if (threadIdx.x == 0) a.join[plan->slot].parts = 0;
+    if (warp == 4) dealloc(*tmem_slot, kTmemColumns);
     return;
   }
-  if (warp == 4) alloc(smem_u32(tmem_slot), kTmemColumns);
-  fence_before();
-  __syncthreads();
-  fence_after();
   const int G = a.group;
   // Columns of TMEM: S, P, the part of Q kept there, O.  A role reads what it needs of these for
   // itself; held across the split into roles, they were spilled in all of them.
@@ -916,7 +943,6 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
   } else if (warp < 7) {
     // ---------------- copying warps: warp 5 K, warp 6 V ----------------
     const bool is_v = warp == 6;
-    const int r0 = *row_tile * kTileRows;
     // one row tile: the cache is read once, its L2 lines go first; several: the row tiles of
     // a pair share them
     uint64_t pol;
@@ -930,30 +956,7 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
     const uint32_t empty = F8 && is_v ? raw_empty : is_v ? v_empty : k_empty;
     const uint32_t ring = F8 && is_v ? base + Lay::kRawV : is_v ? sV : sK;
     int nseg = 0;
-    Walk *walk = reinterpret_cast<Walk *>(plan->warp_sum);
-    if (warp == 5 && lane == 0) walk->begin(a, *plan);
-    // The next segment: the K warp finds and publishes it and asks for its Q rows, the V warp
-    // takes it from the ring.
-    auto advance = [&]() {
-      if (!is_v && lane == 0) {
-        walk->next(a, plan->m, ring_seg[nseg % kSegRing]);
-        mbar_arrive(seg_full + 8 * (nseg % kSegRing));
-      }
-      __syncwarp();
-      if (!__all_sync(kFullMask, segment(nseg++))) return false;
-      if (is_v) return true;
-#pragma unroll 1
-      for (int r = r0 + lane; r < min(r0 + kTileRows, seg.L * G); r += 32) {
-        const uint16_t *p = a.q + ((size_t)(seg.q0 + r / G) * a.q_heads + seg.g * G + r % G) * D;
-#pragma unroll
-        for (int h = 0; h < H; ++h)
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(p + 64 * h));
-      }
-      return true;
-    };
-    bool more = advance();
-    int aj = seg.j0, issued = 0, slot_in = 0;
-    uint32_t empty_parity = 1;  // of the ring's previous round
+    int aj = 0;
     // The table's entry of key tile j for this lane's block (`held`: not past the context).
     // Read one tile before it is looked at, so that nothing waits for the load.
     bool held = false;
@@ -963,7 +966,21 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
       held = lane < kTileBlocks && tok < seg.ctx;
       if (held) next_blk = a.block_tables[(size_t)seg.s * a.max_blocks + tok / kBlockSize];
     };
-    if (more) read_block(aj);
+    // The next segment: the K warp finds and publishes it, both take it from the ring.
+    auto advance = [&]() {
+      if (!is_v && lane == 0) {
+        walk_of(plan)->next(a, plan->m, ring_seg[nseg % kSegRing]);
+        mbar_arrive(seg_full + 8 * (nseg % kSegRing));
+      }
+      __syncwarp();
+      if (!__all_sync(kFullMask, segment(nseg++))) return false;
+      aj = seg.j0;
+      read_block(aj);
+      return true;
+    };
+    bool more = advance();
+    int issued = 0, slot_in = 0;
+    uint32_t empty_parity = 1;  // of the ring's previous round
     // Queues the run's next tile once its slot is free; false: gave up.
     auto issue = [&]() {
       int blk = held ? next_blk : -1;
@@ -972,11 +989,10 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
         flag_error(a.err, PKV_DEV_BAD_BLOCK);
         blk = -1;
       }
-      if (++aj >= seg.j1) {
+      if (++aj < seg.j1)
+        read_block(aj);  // one tile ahead
+      else
         more = advance();
-        aj = seg.j0;
-      }
-      if (more) read_block(aj);  // one tile ahead
       if (issued >= slots && !mbar_wait(empty + 8 * slot_in, empty_parity, abort_flag, a.err))
         return false;
       if (lane < kTileBlocks) {
