@@ -345,12 +345,14 @@ int rope_impl(RopeArgs &a, const uint8_t *pair_axis, int num_axes, int rotary_di
   a.num_slots = (int64_t)num_blocks * kBlockSize;
   const int rows = a.q_heads + 2 * a.kv_heads;
   const int groups = kRopeThreads * 8 / head_dim;
-  // Many tokens: kMaxTile per CTA, every head (a token's sines are made once).  Fewer: one token
-  // per CTA, its rows split over CTAs until there are as many as fit at once or a lane group has
-  // one row (400 tokens, 64/8 heads, E4M3: 11.2 us with four CTAs per SM, 6.5 with eight, 8.5
-  // with sixteen).
+  // Many tokens: kMaxTile per CTA, every head (a token's sines are made once; one / two a CTA:
+  // head_dim 64, 2432 tokens 7.1 / 5.6 us, 16384 tokens 45 / 40; head_dim 128, E4M3, 2500 tokens
+  // 29 / 33, where two leave a short last wave, 3648 tokens 40 / 40, 16384 156 / 150).  Fewer: one
+  // token per CTA, its rows split over CTAs until there are as many as fit at once or a lane
+  // group has one row (400 tokens, 64/8 heads, E4M3: 11.2 us with four CTAs per SM, 6.5 with
+  // eight, 8.5 with sixteen).
   const int sms = device_sm_count();
-  a.tile = a.num_tokens >= 16 * sms ? kMaxTile : 1;
+  a.tile = a.num_tokens >= (head_dim == 64 ? 8 : 24) * sms ? kMaxTile : 1;
   int parts = 1;
   if (a.tile == 1) {
     parts = kRopeCtas * sms / a.num_tokens;

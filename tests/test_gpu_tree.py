@@ -157,6 +157,14 @@ def test_qk_norm_rope_write(ops, f8, T, Hq, Hkv, D, rot, axes, order, inter, nor
 
 
 @pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("T,D", [(1215, 64), (1217, 64), (3647, 128), (3651, 128), (400, 128)])
+@pytest.mark.parametrize("inter", [False, True])
+def test_qk_norm_rope_write_around_the_launch_shapes(ops, f8, T, D, inter):
+    """One and two tokens per CTA, and a token's heads over several CTAs."""
+    test_qk_norm_rope_write(ops, f8, T, 12, 2, D, 32, 1, None, inter, True, 1.0)
+
+
+@pytest.mark.parametrize("f8", [False, True])
 def test_write_without_norm_or_rotation_is_the_plain_write(ops, f8):
     g, qkv, NB, slots, _, _, _ = rope_case(50, 4, 2, 128, 5)
     dq = qkv.cuda()
