@@ -305,6 +305,28 @@ def test_attention_many_sequences_heads_and_row_tiles(ops, lens, Hq, Hkv, D, max
 
 
 @pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("lens,Hq,Hkv,D", [
+    # one row tile more than a launch takes: the second launch has a single one
+    ([(80, 5), (930, 920)], 9, 1, 64),
+    # row tiles of very different lengths, none of them shared
+    ([(4000, 8), (20, 17), (600, 40), (33, 33), (2500, 1)], 8, 1, 128),
+    # empty sequences between the others
+    ([(0, 0), (700, 8), (64, 0), (5, 5), (0, 0), (129, 3)], 8, 8, 64),
+    # as many sequences as a warp, a CTA and a CTA with one more have threads
+    ([(40 + s % 60, 1 + s % 2) for s in range(256)], 2, 1, 64),
+    ([(40 + s % 60, 1 + s % 2) for s in range(385)], 2, 1, 64),
+])
+def test_attention_cut_into_runs(ops, lens, Hq, Hkv, D, f8):
+    w = Tree(lens, Hq, Hkv, D, seed=Hq, f8=f8)
+    out, d = run_tree(ops, w)
+    ref, bound = w.attention64()
+    assert_within(out, ref, bound)
+    assert int(d["err"]) == 0
+    again, _ = run_tree(ops, w, d=d)
+    assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("f8", [False, True])
 def test_attention_arbitrary_masks(ops, f8):
     """Masks that are no tree: random bits, rows that see nothing of the tree, a whole tree
     with no context and empty rows (zeros), bits past the tree's end, more words than
