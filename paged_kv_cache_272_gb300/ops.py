@@ -485,6 +485,7 @@ _BF16, _U8, _I32, _I64T, _F32, _F64 = (torch.bfloat16, torch.uint8, torch.int32,
                                        torch.float32, torch.float64)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _fits(index, dtype, tensors):
@@ -518,9 +519,9 @@ def _run(call, fn, index, stream, err_flag, *args):
     object of that device, or a handle) or that device's current stream."""
     err = None
     if err_flag is not None:
-        if err_flag.dtype is not _I32 or err_flag.get_device() != index or err_flag.numel() < 1:
+        err = err_flag.data_ptr()  # 0: no elements
+        if not err or err_flag.dtype is not _I32 or err_flag.get_device() != index:
             raise TypeError(f"{call}: err_flag must be an int32 tensor on cuda:{index}")
-        err = err_flag.data_ptr()
     if stream is None:
         stream = _raw_stream(index)
     elif hasattr(stream, "cuda_stream"):
@@ -528,7 +529,7 @@ def _run(call, fn, index, stream, err_flag, *args):
             raise ValueError(f"{call}: the stream is on {stream.device}, the tensors on "
                              f"cuda:{index}")
         stream = stream.cuda_stream
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         code = fn(*args, err, stream)
     else:
         with torch.cuda.device(index):
