@@ -1103,7 +1103,7 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
 
 // Joins the parts of a (sequence, KV head, row tile) whose key tiles several CTAs ran: part 0
 // is the last segment of CTA b, part k > 0 the first segment of CTA b + k.
-//   M = max lse_k,  out = sum_k 2^(lse_k - M) o_k / sum_k 2^(lse_k - M)
+//   M = max lse_k,  out = sum_k 2^(lse_k - M) o_k / sum_k 2^(lse_k - M)   over lse_k > -inf
 // A thread has one row and four head-dim columns at a time, a warp 32 adjacent rows: its loads
 // are whole lines, just written and still in L2.  What costs is the round trips (the record,
 // then the weights, then the values), so the first two parts' are asked for with the record:
@@ -1147,22 +1147,32 @@ __global__ void __launch_bounds__(kMergeThreads)
   float4 o[kCols];
 #pragma unroll
   for (int c = 0; c < kCols; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](float w, const float4(&v)[kCols]) {
+  auto add = [&](float x, const float4(&v)[kCols]) {
+    const float w = exp2f(x - ref);
     L += w;
-    if (w != 0.f)  // a part that saw nothing, or whose weight vanishes, adds nothing
+    if (w != 0.f) {
 #pragma unroll
       for (int c = 0; c < kCols; ++c)
         o[c] = make_float4(fmaf(w, v[c].x, o[c].x), fmaf(w, v[c].y, o[c].y),
                            fmaf(w, v[c].z, o[c].z), fmaf(w, v[c].w, o[c].w));
+    } else if (x != -INFINITY) {
+      // a weight that vanishes in fp32 but is above zero: of its values those that are not
+      // finite count (a part that saw nothing, lse -inf, adds nothing)
+      auto odd = [](float e) { return fabsf(e) < INFINITY ? 0.f : e; };
+#pragma unroll
+      for (int c = 0; c < kCols; ++c)
+        o[c] = make_float4(o[c].x + odd(v[c].x), o[c].y + odd(v[c].y), o[c].z + odd(v[c].z),
+                           o[c].w + odd(v[c].w));
+    }
   };
-  add(exp2f(x0 - ref), v0);
-  add(exp2f(x1 - ref), v1);
+  add(x0, v0);
+  add(x1, v1);
 #pragma unroll 4
   for (int k = 2; k < it.parts; ++k) {
     float4 v[kCols];
 #pragma unroll
     for (int c = 0; c < kCols; ++c) v[c] = value(k, c);
-    add(exp2f(__ldcg(lse + slot(k) * kTileRows) - ref), v);
+    add(__ldcg(lse + slot(k) * kTileRows), v);
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
   uint16_t *out = a.out + ((size_t)(it.q0 + r / G) * a.q_heads + it.g * G + r % G) * D + 4 * c0;
