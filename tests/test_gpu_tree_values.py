@@ -1,4 +1,6 @@
-"""Tree attention where values or scores are unusual."""
+"""Tree attention where values or scores are unusual: V elements that are not finite under a
+finite score, in short contexts (one CTA) and long ones (parts that are joined), scores far
+apart, queries with an outlier channel, caches past 2^31 bytes."""
 import copy
 
 import numpy as np
@@ -21,6 +23,10 @@ def _need_gpu():
 def ops():
     from paged_kv_cache_272_gb300 import ops as o
     return o
+
+
+def i32(a):
+    return torch.as_tensor(np.asarray(a, np.int32), device="cuda")
 
 
 def set_v(w, s, t, head, d, value):
@@ -80,6 +86,21 @@ INF, NAN = float("inf"), float("nan")
 
 @pytest.mark.parametrize("f8", [False, True])
 @pytest.mark.parametrize("lens,Hq,Hkv,D", [
+    ([(150, 40), (30, 30), (200, 70)], 8, 4, 64),  # a tree inside one or two tiles
+    ([(700, 300)] * 12, 16, 16, 64),               # several tree tiles of one CTA's run
+    ([(700, 300)] * 6, 16, 16, 128),
+    ([(6000, 300)], 4, 2, 128),                    # parts of one to a few tiles, joined
+    ([(6000, 300), (4100, 20)], 4, 2, 64),
+])
+def test_values_not_finite_under_finite_scores(ops, lens, Hq, Hkv, D, f8):
+    w = Tree(lens, Hq, Hkv, D, seed=50 + len(lens), f8=f8)
+    odd = odd_values(w, (0, 3, 63, 64, 130, 199, 255, 256, 299), [NAN] if f8 else [INF, -INF, NAN])
+    n = check_odd_values(ops, w, odd)
+    assert 0 < n < w.q.numel() // 10
+
+
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("lens,Hq,Hkv,D", [
     ([(400, 20)], 4, 2, 64),     # few parts
     ([(9000, 100)], 8, 2, 128),  # many
 ])
@@ -102,3 +123,83 @@ def test_values_not_finite_under_vanishing_weights(ops, lens, Hq, Hkv, D, f8):
     assert w.scale * 1024 * 7 > 600
     odd = odd_values(w, (0, 7, 19, 40, 63, 64, 99), [NAN] if f8 else [INF, -INF, NAN], seed=1)
     assert check_odd_values(ops, w, odd) > 0
+
+
+def split_error(w):
+    """How far E4M3 scores may be off by the two-term form of q: it is exact for elements down
+    to 2^-9 of the row's largest, and within 2^-17 of the largest below."""
+    q = w.q.double().abs()
+    top = q.amax(-1, keepdim=True)
+    err = torch.where(q < top * 2.0 ** -9, top * 2.0 ** -17, torch.zeros_like(q))
+    worst = torch.zeros(w.q.shape[0], w.Hq, dtype=torch.float64)
+    G = w.Hq // w.Hkv
+    for s in range(w.S):
+        k, _ = w.kv64(s)
+        rows = slice(int(w.qs[s]), int(w.qs[s + 1]))
+        e = err[rows].view(-1, w.Hkv, G, w.D)
+        worst[rows] = torch.einsum("nhgd,chd->nhgc", e, k.abs()).amax(-1).reshape(-1, w.Hq)
+    return worst * w.scale
+
+
+def check_scores(ops, w):
+    out, d = run_tree(ops, w)
+    ref, bound = w.attention64()
+    n = int(w.qs[-1])
+    if w.f8:
+        # a score off by e moves a weight by e of itself and the sum as much; |out| <= max |V|
+        vmax = max(float(w.kv64(s)[1].abs().max()) for s in range(w.S))
+        bound = bound + (2 * split_error(w)[:n, :, None] * vmax)
+    assert_within(out[:n], ref, bound)
+    assert int(d["err"]) == 0
+
+
+@pytest.mark.parametrize("lens", [[(700, 30)], [(5000, 30)], [(2000, 5)] * 40])
+@pytest.mark.parametrize("D", [64, 128])
+def test_e4m3_scores_far_apart(ops, lens, D):
+    """The running maximum jumps by tens to hundreds, early and late in a run."""
+    w = Tree(lens, 8, 2, D, seed=60, f8=True)
+    # scores up to ~150, their fp32 rounding below 2^-24 x 2^13: inside the bound's 2^-10
+    w.q = (w.q.float() * 40).to(torch.bfloat16)
+    check_scores(ops, w)
+
+
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("lens", [[(333, 40), (64, 64)], [(5000, 9)]])
+def test_queries_with_an_outlier_channel(ops, lens, f8):
+    w = Tree(lens, 8, 2, 128, seed=61, f8=f8)
+    w.q[:, :, 17] *= 60
+    w.q[::3, :, 90] *= 2.0 ** -12
+    check_scores(ops, w)
+
+
+def test_e4m3_cache_offsets_past_32_bits(ops):
+    """Blocks at the far end of E4M3 caches of more than 2^31 bytes: written, read, moved."""
+    Hkv, D = 8, 128
+    w = Tree([(200, 20), (90, 7)], 8, Hkv, D, seed=15, f8=True, poison=False)
+    NB = 2**31 // (Hkv * BS * D) + 40
+    if torch.cuda.mem_get_info()[0] < 4 * NB * Hkv * BS * D:
+        pytest.skip("not enough free memory")
+    d = w.cuda()
+    far = torch.arange(w.NB, device="cuda") + NB - w.NB
+    for n in ("k", "v"):
+        big = torch.empty(NB, Hkv, BS, D, dtype=torch.uint8, device="cuda")
+        big[far] = d[n]
+        d[n] = big
+    d["bt"] = torch.where(d["bt"] >= 0, d["bt"] + NB - w.NB, d["bt"])
+    out, _ = run_tree(ops, w, d=d)
+    ref, bound = w.attention64()
+    assert_within(out, ref, bound)
+    assert int(d["err"]) == 0
+    slots = d["slots"] + (NB - w.NB) * BS
+    v = d["v"].view(NB, Hkv, D, BS)
+    take = lambda i: (d["k"][slots[i] // BS, :, slots[i] % BS].clone(),
+                      v[slots[i] // BS, :, :, slots[i] % BS].clone())
+    want = take(19)
+    ops.paged_tree_commit_fp8(d["k"], d["v"], slots, d["qs"], i32([[19, 3], [0, 6]]), i32([2, 2]))
+    assert all(torch.equal(a, b) for a, b in zip(take(0), want))
+    rows = torch.randn(27, 16, D, device="cuda").to(torch.bfloat16)
+    ops.paged_qk_norm_rope_write_fp8(rows[:, :8].clone(), rows[:, :8], rows[:, 8:], rows[:, 8:],
+                                     None, None, slots, d["k"], d["v"], 1.0, 1.0)
+    codes = rows[:, 8:].to(torch.float8_e4m3fn).view(torch.uint8)
+    assert torch.equal(d["k"][slots // BS, :, slots % BS], codes)
+    assert torch.equal(v[slots // BS, :, :, slots % BS], codes)
