@@ -74,6 +74,11 @@ constexpr int kStart = 5, kStartF8 = 12;
 // Least units of a run: one sequence of 700 tokens takes 14.6 us with runs of 3, 14.0 with 4
 // (fewer parts to join), 14.5 with 5, 15.2 with 6.
 constexpr int kMinRun = 4;
+// E4M3: a weight enters its product as f16 of 2^kLift times itself, so that one of 2^-21 of the
+// row's largest still has all of f16's bits and none above 2^-32 is lost (the sum keeps them all:
+// unlifted, the part of a run's keys below 2^-25 each vanished from the result, a percent of it
+// at half a million keys).  The lagging reference lets weights grow by 2^8: at most 2^15.
+constexpr float kLiftF8 = 7.f;
 
 struct TreeArgs {
   uint16_t *out;                // [T][Hq][D] bf16
@@ -463,6 +468,7 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
                           const __grid_constant__ CUtensorMap tv) {
   using Lay = TreeLayout<D, F8>;
   constexpr int H = Lay::kHalves, KS = Lay::KS, VS = Lay::VS, RS = Lay::RS;
+  constexpr float kLift = F8 ? kLiftF8 : 0.f;
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t base = smem_u32(smem);
   if (base & 1023u) {  // the swizzled tiles need a 1024-byte aligned window
@@ -704,7 +710,7 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
             }
           }
           // a row that has seen nothing yet: every weight 2^-inf = 0
-          const float ref = m == -INFINITY ? 0.f : m;
+          const float ref = (m == -INFINITY ? 0.f : m) - kLift;
           uint64_t ps2[4];
           const uint64_t sl2 = f32x2(sl, sl), nm2 = f32x2(-ref, -ref);
 #pragma unroll
@@ -716,7 +722,9 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
             const float p0 = ex2(e0), p1 = ex2(e1);
             const uint64_t pp = f32x2(p0, p1);
             ps2[c & 3] = c < 4 ? pp : add_f32x2(ps2[c & 3], pp);
-            // the product takes 16-bit weights; the sum keeps them in fp32
+            // The product takes 16-bit weights (the sum keeps them in fp32): bf16 beside bf16
+            // V, half a step 2^-9 of each, as much as the output's own rounding; f16 beside
+            // E4M3 codes, 2^-12 of each down to kLift's floor.
             pk[c] = F8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
           }
           float s0, s1;

@@ -203,3 +203,36 @@ def test_e4m3_cache_offsets_past_32_bits(ops):
     codes = rows[:, 8:].to(torch.float8_e4m3fn).view(torch.uint8)
     assert torch.equal(d["k"][slots // BS, :, slots % BS], codes)
     assert torch.equal(v[slots // BS, :, :, slots % BS], codes)
+
+
+def test_e4m3_long_tail_of_small_weights(ops):
+    """One token that outweighs each of half a million others by 2^25.3: their share of the
+    result, 1.2 percent, is not lost.  Every CTA's run is one whole sequence (all share the
+    same few blocks), so that one reference serves all of its keys."""
+    n, D, x = 1 << 19, 64, 25.3
+    S = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    z = lambda *s, t=torch.int32: torch.zeros(*s, dtype=t, device="cuda")
+    k, v = z(2, 1, BS, D, t=torch.uint8), z(2, 1, BS, D, t=torch.uint8)
+    one = int(torch.tensor(1.0).to(torch.float8_e4m3fn).view(torch.uint8))
+    k[0, 0, 0, 0] = one  # the token that outweighs: score q . K = 1, the others' 0; V 0, theirs 1
+    v.view(2, 1, D, BS)[:] = one
+    v.view(2, 1, D, BS)[0, 0, :, 0] = 0
+    bt = z(S, n // BS).fill_(1)
+    bt[:, 0] = 0
+    q = z(S, 1, D, t=torch.bfloat16)
+    q[..., 0] = 1
+    out, err = torch.empty_like(q), z(1)
+    ws = ops.alloc_tree_workspace(1, 1, D, 1)
+    masks = torch.ones(S, 1, dtype=torch.int64, device="cuda")
+    ops.paged_attention_tree_fp8(out, q, k, v, bt, z(S).fill_(n),
+                                 torch.arange(S + 1, dtype=torch.int32, device="cuda"), masks,
+                                 x * np.log(2.0), 1.0, 1.0, 1, ws, err_flag=err)
+    w = (n - 1) * 2.0 ** -x
+    want = w / (1 + w)
+    # bf16's half step; a weight of 2^-25.3 lifted by 2^7 is within 2^-25 in f16 (2^-32 of the
+    # largest); the product's sum grows by 4 x 8192 terms of equal size, each truncated to 2^-23
+    # of what has been summed (2^-24 on average); l, above 2^7, takes 8192 terms within 2^-17
+    tol = want * (2.0 ** -8 + 2.0 ** -9 + 2.0 ** -11) + n * 2.0 ** -32
+    assert tol < want / 20
+    assert int(err) == 0
+    assert float((out.double() - want).abs().max()) <= tol
