@@ -472,7 +472,14 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t base = smem_u32(smem);
   if (base & 1023u) {  // the swizzled tiles need a 1024-byte aligned window
-    if (threadIdx.x == 0) flag_error(a.err, PKV_DEV_LAYOUT);
+    // Every CTA of the launch comes here or none does, so each slot of the workspace gets its
+    // word for the join: nothing to do.
+    pdl_trigger();
+    pdl_wait();
+    if (threadIdx.x == 0) {
+      flag_error(a.err, PKV_DEV_LAYOUT);
+      a.join[blockIdx.x].parts = 0;
+    }
     return;
   }
   const uint32_t sQ = base + Lay::kQ, sK = base + Lay::kK, sV = base + Lay::kV;
