@@ -369,17 +369,18 @@ int paged_tree_masks(uint64_t *masks, int32_t *positions, const int32_t *parents
  *   t = positions[pair_axis[i]][t] * inv_freq[i]
  * with pairs (y[i], y[i + rotary_dim/2]), or (y[2i], y[2i+1]) with interleaved != 0;
  * elements at or past rotary_dim pass.  v is written as it is.  Computed in fp32 and rounded
- * once.  Angles: a pair's turns per position are held to 64 bits after the point, so any int32
- * position's are exact to 2^-33 of a turn beyond inv_freq's own rounding.
+ * once.  Angles: a pair's turns per position are held to 64 bits after the point, so for any
+ * int32 position the product is within 2^-33 + |inv_freq| 2^-41 of a turn of the given
+ * inv_freq's; sine and cosine are taken of the 24 bits an fp32 value keeps of its fraction.
  * q, k, v, q_out: head rows of head_dim elements, heads adjacent, tokens *_stride elements
  * apart (multiples of 8, at least the row of heads), so they may be slices of one packed
  * projection.  q_out may be q itself (same address and stride); other overlap is not
  * allowed.  positions: int32, axis a of token t at a * axis_stride + t (axis_stride 0: all
  * axes share them).  num_axes 1..4.  pair_axis: HOST array of rotary_dim/2 bytes, read
  * during the call (NULL: axis 0; an entry >= num_axes returns PKV_ERR_ARG).  inv_freq: fp64
- * device array of rotary_dim/2 radians per position, finite and below 2^53.  rotary_dim: 0 or a multiple of 16 up
- * to head_dim; head_dim 64 or 128.  A negative slot writes no k and v (q_out is written); a
- * slot outside the pool sets PKV_DEV_BAD_SLOT and does the same.
+ * device array of rotary_dim/2 radians per position, finite and below 2^53.  rotary_dim: 0 or
+ * a multiple of 16 up to head_dim; head_dim 64 or 128.  A negative slot writes no k and v
+ * (q_out is written); a slot outside the pool sets PKV_DEV_BAD_SLOT and does the same.
  */
 int paged_qk_norm_rope_write(uint16_t *q_out, int64_t q_out_stride, const uint16_t *q,
                              int64_t q_stride, const uint16_t *k, int64_t k_stride,

@@ -7,11 +7,12 @@
 // (y[2 i], y[2 i + 1]) when interleaved.  All of it in fp32 with one rounding at the store
 // (bf16, or the E4M3 code of value / scale).  v is stored as it is.
 //
-// Angles: a turn count t / 2 pi needs its fraction only, so a frequency is held as a 64-bit
+// Angles: a turn count t / 2 pi needs its fraction only, so a frequency w is held as a 64-bit
 // fixed-point fraction of a turn per position and multiplied by the 32-bit position modulo
-// 2^64: the angle's error is that of the frequency's own rounding (2^-53) times the
-// position, however far the position -- where an fp32 product would be 0.06 rad off at a
-// million.  sincospi then takes the top bits.
+// 2^64.  The fraction is within 2^-64 (its truncation) + w 2^-72 (that of the 64 bits of 2 / pi)
+// of a turn, the product of any position within 2^-33 + w 2^-41 -- where an fp32 product would
+// be 0.06 rad off at a million.  Its top 32 bits, rounded to a float (2^-26 of a turn at most),
+// go to sincospi.
 //
 // Layout: D / 8 lanes own a (token, head) row.  A rotating lane holds four elements of each
 // half (half-split pairs) or four adjacent pairs, so both elements of a pair meet in one lane
