@@ -425,10 +425,10 @@ size_t paged_attention_tree_workspace_size(int num_q_heads, int num_kv_heads, in
  * over those t, as paged_attention_prefill computes it (scale > 0).  A row that sees no
  * token gives zeros.  A token that a row does not see takes no part in it, whatever its K
  * and V rows hold.  The drafts' K/V must be in the cache.  max_query_len: host bound of
- * every L, at most 64 mask_words (0: nothing is queued).  A sequence with L > max_query_len, L > context_lens[s], a
- * context beyond its block table or rows outside [0, num_tokens] sets PKV_DEV_BAD_CONTEXT
- * and its rows are left unwritten; a bad block id sets PKV_DEV_BAD_BLOCK and the rows of its
- * sequence are unspecified.  L == 1 with bit 0 is a decode row.  The key range of one
+ * every L, at most 64 mask_words (0: nothing is queued).  A sequence with L > max_query_len,
+ * L > context_lens[s], a context beyond its block table or rows outside [0, num_tokens] sets
+ * PKV_DEV_BAD_CONTEXT and its rows are left unwritten; a bad block id sets PKV_DEV_BAD_BLOCK and
+ * the rows of its sequence are unspecified.  L == 1 with bit 0 is a decode row.  The key range of one
  * sequence is split over CTAs and joined; the result does not depend on timing.
  * workspace: as paged_attention_decode's (256-byte aligned scratch, no initialisation; calls
  * that share one must be ordered).  head_dim 64 or 128, num_seqs <= 65535.
@@ -444,8 +444,9 @@ int paged_attention_tree(uint16_t *out, const uint16_t *q, const uint16_t *k_cac
 
 /* The same over E4M3 caches (q enters the score product as the sum of two E4M3 terms under a
  * power of two per row, exact for elements down to 2^-9 of the row's largest; the weights
- * enter theirs as f16).  Scales as in paged_decode_step_fp8; a per-head scale that is
- * not > 0 sets PKV_DEV_BAD_SCALE and the rows reading that head are unspecified. */
+ * enter theirs as f16, to 2^-11 of each and none above 2^-32 of the largest lost).  Scales as in
+ * paged_decode_step_fp8; a per-head scale that is not > 0 sets PKV_DEV_BAD_SCALE and the rows
+ * reading that head are unspecified. */
 int paged_attention_tree_fp8(uint16_t *out, const uint16_t *q, const uint8_t *k_cache,
                              const uint8_t *v_cache, const int32_t *block_tables,
                              const int32_t *context_lens, const int32_t *query_start,

@@ -19,8 +19,11 @@
 // and nothing is exchanged but the norm's sum; its four sines stay in registers for all the
 // heads it serves.  Two rows are in flight behind the one being worked on.
 //
-// Bound: bytes, with the instruction issue close behind (16 bytes a lane and row), hence the
-// packed arithmetic and the division below.
+// Bound: for prompts latency at this occupancy (16384 tokens of head_dim 64: DRAM 49% busy, 2.3 of
+// 4 instructions issued a cycle, 45% of the warps resident), 1.36 times the bytes' time; hence the
+// rows in flight, the packed arithmetic and the division below.  E4M3 (16384 tokens, 64/8 heads of
+// 128: 149 us for 94 of bytes) has V's codes besides, stored a byte at a time into the transposed
+// blocks.
 #include <math.h>
 
 #include <cstring>
@@ -347,11 +350,11 @@ int rope_impl(RopeArgs &a, const uint8_t *pair_axis, int num_axes, int rotary_di
   const int rows = a.q_heads + 2 * a.kv_heads;
   const int groups = kRopeThreads * 8 / head_dim;
   // Many tokens: kMaxTile per CTA, every head (a token's sines are made once; one / two a CTA:
-  // head_dim 64, 2432 tokens 7.1 / 5.6 us, 16384 tokens 45 / 40; head_dim 128, E4M3, 2500 tokens
-  // 29 / 33, where two leave a short last wave, 3648 tokens 40 / 40, 16384 156 / 150).  Fewer: one
-  // token per CTA, its rows split over CTAs until there are as many as fit at once or a lane
-  // group has one row (400 tokens, 64/8 heads, E4M3: 11.2 us with four CTAs per SM, 6.5 with
-  // eight, 8.5 with sixteen).
+  // head_dim 64, 32/8 heads, 2432 tokens 7.9 / 6.9 us, 16384 tokens 45 / 40; head_dim 128, 64/8
+  // heads, E4M3, 1021 tokens 15 / 25 and 2500 tokens 31 / 35, where two leave a short last wave,
+  // 3648 tokens 40 / 40, 16384 155 / 149).  Fewer: one token per CTA, its rows split over CTAs
+  // until there are as many as fit at once or a lane group has one row (400 tokens, 64/8 heads,
+  // E4M3: 11.2 us with four CTAs per SM, 6.5 with eight, 8.5 with sixteen).
   const int sms = device_sm_count();
   a.tile = a.num_tokens >= (head_dim == 64 ? 8 : 24) * sms ? kMaxTile : 1;
   int parts = 1;

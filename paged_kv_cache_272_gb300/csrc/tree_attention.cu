@@ -23,15 +23,17 @@
 //
 // Split.  With few rows the work is reading the cache, and a batch may be one long sequence
 // or many short ones.  So the key tiles of all (sequence, KV head) pairs of a row tile are
-// laid end to end and cut into equal runs, one per resident CTA: every CTA reads the same
-// amount, whatever the lengths.  A pair cut by a run's end leaves normalised fp32 partial
-// results (at most two per CTA, so the workspace does not grow with the batch) that
-// tree_merge_kernel joins by their log-sum-exp in the order of the keys; nothing is summed
-// in an order that depends on timing.  Each CTA finds its run from context_lens by itself:
+// laid end to end, a few units for each pair's start before its tiles, and cut into runs of
+// equal length, one per resident CTA.  Long pairs so give every CTA about as many tiles; where a
+// pair has about as many tiles as start units, a run can fall within the latter and have none.
+// A pair cut by a run's end leaves normalised fp32 partial results (at most two per CTA, so the
+// workspace does not grow with the batch) that tree_merge_kernel joins by their log-sum-exp in
+// the order of the keys; nothing is summed in an order that depends on timing.  Each CTA finds its run from context_lens by itself:
 // one launch for the attention, one for the join.  The row tiles of a pair are run by
 // neighbouring CTAs, which start together and stay near enough for the cache to come from DRAM
-// once and from L2 for the others (eight sequences of 65536 tokens, three row tiles: 703 us;
-// 776 with one row tile's CTAs after the other's, which drift apart by more than L2 holds).
+// once and from L2 for the others (eight sequences of 65536 tokens, three row tiles: 676-701 us;
+// with one row tile's CTAs after the other's, which drift apart by more than L2 holds, 776 beside
+// 705).
 //
 // Masked values.  A weight of zero times a V element that is not finite would spoil a row
 // that does not see it.  Tiles that overlap the tree (every row sees the others) are checked:
@@ -60,19 +62,19 @@ constexpr int kTileBlocks = kTileKeys / kBlockSize;
 // Threads per CTA: warps 0-3 softmax, 4-7 products and copies, 8-11 (E4M3) widening.
 __host__ __device__ constexpr int tree_threads(bool f8) { return f8 ? 384 : 256; }
 // E4M3: 384 threads of 80 registers, twice per SM; the softmax warps take 160 and the others
-// leave 40 (128 x 160 + 256 x 40 = 384 x 80).  Batch of 64: 182 us with 128 / 56, 173 with
-// 144 / 48, 169 with 160 / 40.
+// leave 40 (128 x 160 + 256 x 40 = 384 x 80).  Batch of 64: 170.7 us with 128 / 56, 166.7 with
+// 144 / 48, 166.1 with 160 / 40.  24 bytes are spilled and 36 read back.
 constexpr int kLaunchRegs = 80, kSoftmaxRegs = 160, kOtherRegs = 40;
 static_assert(128 * kSoftmaxRegs + 256 * kOtherRegs <= 384 * kLaunchRegs, "register split");
 constexpr uint32_t kTmemColumns = 256;
 constexpr int kMaxRowTiles = 64;  // row tiles of one launch
-// A segment's start and finish, in key tiles.  Measured, 3 / 4 / 5 / 6: 32 ragged sequences 77.9 /
-// 77.1 / 77.2 / 76.5 us, short MHA contexts 24.2 / 24.2 / 23.8 / 24.8; E4M3, 64 ragged
-// sequences, 6 / 8 / 10 / 12: 170 / 169 / 169 / 167 (q's two terms take longer to make).  None
-// at all: 79, 29, 186 (before other changes).
+// A segment's start and finish, in key tiles.  Measured, 3 / 4 / 5 / 6: 32 ragged sequences 77.5 /
+// 76.6 / 76.1 / 76.0 us, short MHA contexts 23.8 / 23.6 / 23.4 / 24.2; E4M3, 64 ragged sequences,
+// 4 / 6 / 8 / 10 / 12: 170.1 / 168.0 / 167.2 / 167.3 / 166.1 (q's two terms take longer to make),
+// while pairs of 12 tiles (38 sequences, 4 KV heads), whose runs are short, take 31-33 with any.
 constexpr int kStart = 5, kStartF8 = 12;
-// Least units of a run: one sequence of 700 tokens takes 14.6 us with runs of 3, 14.0 with 4
-// (fewer parts to join), 14.5 with 5, 15.2 with 6.
+// Least units of a run: one sequence of 700 tokens takes 14.3 us with runs of 3, 12.9 with 4
+// (fewer parts to join), 13.7 with 5, 14.4 with 6.
 constexpr int kMinRun = 4;
 // E4M3: a weight enters its product as f16 of 2^kLift times itself, so that one of 2^-21 of the
 // row's largest still has all of f16's bits and none above 2^-32 is lost (the sum keeps them all:
@@ -730,8 +732,8 @@ __global__ void __launch_bounds__(tree_threads(F8), 2)
             const uint64_t pp = f32x2(p0, p1);
             ps2[c & 3] = c < 4 ? pp : add_f32x2(ps2[c & 3], pp);
             // The product takes 16-bit weights (the sum keeps them in fp32): bf16 beside bf16
-            // V, half a step 2^-9 of each, as much as the output's own rounding; f16 beside
-            // E4M3 codes, 2^-12 of each down to kLift's floor.
+            // V, off by 2^-8 of each at most, as the output's own rounding; f16 beside E4M3 codes,
+            // 2^-11 of each down to kLift's floor.
             pk[c] = F8 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
           }
           float s0, s1;
