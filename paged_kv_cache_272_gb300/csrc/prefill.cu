@@ -503,6 +503,7 @@ __global__ void __launch_bounds__(kTcWarps * 32, 2)
   extern __shared__ __align__(1024) unsigned char smem_tc[];
   const uint32_t base = smem_u32(smem_tc);
   if (base & 1023u) {  // the swizzled tiles need a 1024-byte aligned window
+    pdl_wait();  // the kernel behind this one relies on it
     if (threadIdx.x == 0) flag_error(a.err, PKV_DEV_LAYOUT);
     return;
   }
@@ -909,6 +910,7 @@ __global__ void __launch_bounds__(kTcWarps * 32, 2)
   extern __shared__ __align__(1024) unsigned char smem_tc[];
   const uint32_t base = smem_u32(smem_tc);
   if (base & 1023u) {  // the swizzled tiles need a 1024-byte aligned window
+    pdl_wait();  // the kernel behind this one relies on it
     if (threadIdx.x == 0) flag_error(a.err, PKV_DEV_LAYOUT);
     return;
   }
@@ -1360,6 +1362,7 @@ __global__ void __launch_bounds__(kPairWarps * 32, 1)
   extern __shared__ __align__(1024) unsigned char smem_tc[];
   const uint32_t base = smem_u32(smem_tc);
   if (base & 1023u) {  // the swizzled tiles need a 1024-byte aligned window
+    pdl_wait();  // the kernel behind this one relies on it
     if (threadIdx.x == 0) flag_error(a.err, PKV_DEV_LAYOUT);
     return;
   }
@@ -1896,6 +1899,7 @@ __global__ void __launch_bounds__(kPairCtaWarps * 32, 2)
   // The swizzled tiles need a 1024-byte aligned window; both CTAs run the same code, so
   // a misaligned window is misaligned in both and both leave here.
   if (base & 1023u) {
+    pdl_wait();  // the kernel behind this one relies on it
     if (threadIdx.x == 0) flag_error(a.err, PKV_DEV_LAYOUT);
     return;
   }

@@ -23,7 +23,7 @@ def kernels(name):
         yield m.group(1), text[at:end]
 
 
-@pytest.mark.parametrize("name", ["tree_attention.cu", "tree_masks.cu", "qk_rope.cu"])
+@pytest.mark.parametrize("name", ["tree_attention.cu", "tree_masks.cu", "qk_rope.cu", "prefill.cu"])
 def test_no_kernel_ends_before_it_has_waited_for_the_one_before(name):
     """The kernel behind a dependent launch waits for that launch alone: one that ended without
     waiting would let it start while an older kernel still runs."""
