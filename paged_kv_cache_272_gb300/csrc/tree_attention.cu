@@ -28,9 +28,10 @@
 // pair has about as many tiles as start units, a run can fall within the latter and have none.
 // A pair cut by a run's end leaves normalised fp32 partial results (at most two per CTA, so the
 // workspace does not grow with the batch) that tree_merge_kernel joins by their log-sum-exp in
-// the order of the keys; nothing is summed in an order that depends on timing.  Each CTA finds its run from context_lens by itself:
-// one launch for the attention, one for the join.  The row tiles of a pair are run by
-// neighbouring CTAs, which start together and stay near enough for the cache to come from DRAM
+// the order of the keys; nothing is summed in an order that depends on timing.  Each CTA finds
+// its run from context_lens by itself: one launch for the attention, one for the join.  The row
+// tiles of a pair are run by neighbouring CTAs, which start together and stay near enough for the
+// cache to come from DRAM
 // once and from L2 for the others (eight sequences of 65536 tokens, three row tiles: 676-701 us;
 // with one row tile's CTAs after the other's, which drift apart by more than L2 holds, 776 beside
 // 705).
