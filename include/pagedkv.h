@@ -603,7 +603,7 @@ int paged_tree_commit_fp8(uint8_t *k_cache, uint8_t *v_cache, const int64_t *slo
  * 0 and -1.  target_probs, draft_probs: rows of `vocab` (1 to 2^24) probabilities of prob_bytes
  * bytes (4: fp32, 2: bf16), *_stride elements apart (at least vocab), row query_start[s] + i
  * the distribution after tree token i; a row sums to about 1 (from a sum of 8 on, the token drawn
- * is unspecified, but below vocab).  What is summed is held to 2^-44 each (r to 2^-47 of p), in
+ * is unspecified, but below vocab).  What is summed is held to 2^-43 each (r to 2^-47 of p), in
  * integers: the outputs depend neither on the split nor on timing.  A parent that is not before its child (or not -1 for token 0)
  * sets PKV_DEV_BAD_TREE, a token outside [0, vocab) PKV_DEV_BAD_ROW: it and what hangs under it
  * is not kept (token 0 is, and its id is not looked at).  A probability that was read and is

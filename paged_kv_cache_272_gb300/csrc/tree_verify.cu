@@ -17,8 +17,8 @@
 //
 // Sums.  The sampled token is an integer, looked up where the running sum passes a threshold, so
 // the sums must be good to far less than a token's share and must not depend on how the row is
-// cut: values enter as whole numbers of 2^-44 (p - M d formed as a pair of fp32 numbers, to 2^-47
-// of its terms), and integer sums are the same in any order.  An fp32 number becomes two such
+// cut: values enter as whole numbers of 2^-43 (p - M d formed as a pair of fp32 numbers, to 2^-47
+// of its terms; verify_sum.cuh), and integer sums are the same in any order.  An fp32 number becomes two such
 // integers by adding a constant whose last place is the unit: seven additions a value, where
 // conversions to 64-bit integers took twice the time of everything else (64 trees: 151 us).  No
 // result depends on the cluster's size or on timing.
@@ -29,6 +29,7 @@
 #include <cooperative_groups.h>
 
 #include "pkv_common.cuh"
+#include "verify_sum.cuh"
 
 namespace pkv {
 namespace {
@@ -39,11 +40,6 @@ constexpr int kVerifyThreads = 256, kVerifyWarps = kVerifyThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxVocab = 1 << 24;
 constexpr unsigned kAll = 0xffffffffu;
-// A row's sums, in units of 2^-44: high 2^23 + low, both of 32 bits while the values summed are
-// fewer than 2^9 and sum to less than 2^10.
-constexpr int kUnitBits = 44, kHighBits = 21;
-constexpr float kHighMagic = 12582912.f / (1 << kHighBits);  // 1.5 2^23 units of 2^-21
-constexpr float kLowMagic = 12582912.f / (float)(1ull << kUnitBits);
 constexpr uint32_t kTwo = 0x40000000u;  // 2.f
 
 struct VerifyArgs {
@@ -70,28 +66,6 @@ __device__ __forceinline__ float probability(float v, bool &bad) {
   bad = true;
   return 0.f;
 }
-struct Sum {
-  uint32_t high = 0, low = 0;  // of the magic numbers' bits, modulo 2^32
-  // s + t, |t| at most half a unit in the last place of s, s in [0, 2)
-  __device__ __forceinline__ void add(float s, float t) {
-    const float a = s + kHighMagic, b = ((s - (a - kHighMagic)) + t) + kLowMagic;
-    high += __float_as_uint(a) - __float_as_uint(kHighMagic);
-    low += __float_as_uint(b) - __float_as_uint(kLowMagic);
-  }
-  __device__ __forceinline__ unsigned long long value() const {
-    return ((unsigned long long)(long long)(int)high << (kUnitBits - kHighBits)) +
-           (unsigned long long)(long long)(int)low;
-  }
-};
-// max(p - M d, 0) as a pair of numbers, the product's rounding error carried along.
-__device__ __forceinline__ void residual(float p, float d, float mh, float ml, float &s, float &t) {
-  const float h = mh * d, e = fmaf(ml, d, fmaf(mh, d, -h));
-  s = p - h;
-  const float b = s - p;
-  t = ((p - (s - b)) - (h + b)) - e;
-  if (!(s + t > 0.f)) s = t = 0.f;
-}
-
 template <typename T>
 struct Row {
   static constexpr int W = 16 / (int)sizeof(T);
@@ -389,7 +363,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) tree_verify_kernel(const Ve
       __syncthreads();  // warp_sum has been read
     }
     if (!c.last) {
-      mass = (double)total * 0x1p-44;
+      mass = (double)total / (double)(1ull << kUnitBits);
       continue;
     }
     if (total == 0 && rank == 0 && tid == 0) {
