@@ -811,14 +811,8 @@ int launch_mma_t(const AttnArgs &a, const CUtensorMap &tk, const CUtensorMap &tv
   // CTAs per SM (after opting the kernel into its shared memory on this device)
   static std::atomic<int> occ_slots[kMaxDevices];
   const int occ = per_device_setup(occ_slots, [] {
-    cudaError_t e = cudaFuncSetAttribute(
+    const cudaError_t e = cudaFuncSetAttribute(
         attn_mma_kernel<D, NW, NS, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
-    // the split of the SM's memory of the kernels it runs beside: another one would have to wait
-    // for an empty SM
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(attn_mma_kernel<D, NW, NS, KV8>,
-                               cudaFuncAttributePreferredSharedMemoryCarveout,
-                               (int)cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return -(int)e;
     int n = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_mma_kernel<D, NW, NS, KV8>,
