@@ -52,8 +52,8 @@ struct AttnArgs {
   int32_t *cnt_seq;              // [S][Hq] chunks merged per head (multi-chunk sequences)
   float *chunk_lse;              // [S][max_chunks][Hq]
   float *chunk_o;                // [S][max_chunks][Hq][D]
-  // The launch before runs beside the tensor-core kernel and is waited for at its end: it lets
-  // this one start once the plan is complete (0: waited for at the start).
+  // The launch before runs beside the tensor-core kernel and is waited for at its end: the plan
+  // is complete before that launch starts (0: waited for at the start).
   int beside;
   int32_t *err;
 };

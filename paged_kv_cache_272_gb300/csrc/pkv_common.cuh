@@ -72,10 +72,10 @@ __device__ __forceinline__ uint16_t f32_to_bf16(float f) {
   return *reinterpret_cast<uint16_t *>(&h);
 }
 
-// Programmatic dependent launch.  Every kernel of this library is launched with
-// launch_pdl, so it may become resident while the previous kernel on the stream is
-// still running; it calls pdl_wait() before it touches any memory, which returns once
-// that kernel has completed and its writes are visible (at once when there is no such
+// Programmatic dependent launch.  Every kernel of this library (but those that launch_behind
+// says) is launched with launch_pdl, so it may become resident while the previous kernel on
+// the stream is still running; it calls pdl_wait() before it touches any memory, which returns
+// once that kernel has completed and its writes are visible (at once when there is no such
 // kernel).  pdl_trigger() lets the next kernel start its own launch early.  Only launch
 // latency and prologues overlap; no data dependency is relaxed.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -85,8 +85,8 @@ __device__ __forceinline__ void pdl_trigger() {
 
 #ifdef __CUDACC__
 template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                       cudaStream_t st, Args &&...args) {
+cudaError_t launch_with(int programmatic, void (*kernel)(KArgs...), dim3 grid, dim3 block,
+                        size_t smem, cudaStream_t st, Args &&...args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -96,8 +96,21 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = programmatic;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args &&>(args)...);
+}
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                       cudaStream_t st, Args &&...args) {
+  return launch_with(1, kernel, grid, block, smem, st, static_cast<Args &&>(args)...);
+}
+// An ordinary launch: the kernel starts once everything before it on the stream is complete.
+// What launch_pdl queues behind it starts later still, and may read without pdl_wait() what was
+// complete before this one.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_behind(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                          cudaStream_t st, Args &&...args) {
+  return launch_with(0, kernel, grid, block, smem, st, static_cast<Args &&>(args)...);
 }
 #endif
 

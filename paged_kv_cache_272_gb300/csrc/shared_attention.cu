@@ -367,8 +367,8 @@ __global__ void __launch_bounds__(kJoinThreads, 6)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t row = (int64_t)blockIdx.x * (kJoinWarps / WPR) + warp / WPR;
   const int s = (int)(row / a.q_heads), head = (int)(row % a.q_heads), G = a.group, g = head / G;
-  // (the plan is complete before the launch that this one is behind: read before waiting for that,
-  // past what this SM kept of a plan before)
+  // (the plan is complete before the prefixes' launch starts, and so before this one: read before
+  // waiting for the launch before, past what this SM kept of a plan before)
   __threadfence();
   SeqParts sp = {-1, 0, 0, -1};
   if (row < (int64_t)a.num_seqs * a.q_heads) sp = a.parts[s];
