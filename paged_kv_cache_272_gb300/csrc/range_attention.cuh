@@ -696,7 +696,9 @@ __global__ void __launch_bounds__(threads(F8), 2)
           // amp y P(y^2) of y = in x, by powers of x (E4M3, whose x may be large: of y)
           const float by = F8 ? 1.f : in, by2 = by * by;
           w0 = amp * by, w1 = w0 * by2, w2 = w1 * by2, w3 = w2 * by2;
-          if (by < 0x1p-12f) curve = -1.f;  // powers that fp32 does not hold: the other form
+          // powers that fp32 does not hold, or only as infinity, which times a score of zero is NaN:
+          // the other form
+          if (by < 0x1p-12f || !(w3 <= 0x1p100f)) curve = -1.f;
           w0 *= kTanh0, w1 *= kTanh1, w2 *= kTanh2, w3 *= kTanh3;
         }
         if constexpr (kBias) {
