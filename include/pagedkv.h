@@ -396,8 +396,8 @@ size_t paged_attention_scored_workspace_size(int num_seqs, int num_tokens, int n
  * key_begin = its first position, a part of the prompt that all tokens see key_end = max(p + 1, its
  * length).  A row that sees no key gives zeros.  A key that a row does not see takes no part in it,
  * whatever its K and V rows hold.  Scores, softmax and sums in fp32 (a capped score to 2^-19 of the
- * cap; the bias relative to the row's nearest key, distances exact to 2^24), weights to bf16 for
- * their product.  The new tokens'
+ * cap for caps to 64, to 2^-21 of it above; the bias relative to the row's nearest key, distances
+ * exact to 2^24), weights to bf16 for their product.  The new tokens'
  * K and V must be in the cache.  A sequence with L > context_lens[s], a context beyond its block
  * table or rows outside [0, num_tokens] sets PKV_DEV_BAD_CONTEXT and its rows are left unwritten,
  * as are rows at or past query_start[num_seqs]; a bad block id sets PKV_DEV_BAD_BLOCK and the rows

@@ -75,10 +75,20 @@ constexpr int kMinRun = 4;
 // E4M3: weights enter their product as f16 of 2^kLift times themselves, so that none above 2^-32
 // of the largest is lost.
 constexpr float kLiftF8 = 7.f;
-// tanh(y) / y for |y| <= 0.65, in powers of y^2.
-constexpr float kNearTanh = 0.65f;
-constexpr float kTanh0 = 0.9999839067459106f, kTanh1 = -0.33280691504478455f;
-constexpr float kTanh2 = 0.1286155879497528f, kTanh3 = -0.037672240287065506f;
+// tanh(y) / y for |y| <= near, in powers of y^2 (least largest error of y times it).  To a cap of 64:
+// off by 2^-19.7 of the cap, 2^-13.7 at most in the exponent, far below a weight's rounding, and most
+// tiles of usual scores take it.  Above, where that is up to 0.005: the first power is 1, so that
+// scores far below the cap stay what they are, and it is off by 2^-23.6 of the cap.
+struct TanhFit {
+  float near, c[4];
+};
+constexpr float kFineCap = 64.f;
+inline TanhFit tanh_fit(float cap) {
+  return cap <= kFineCap ? TanhFit{0.65f, {0.9999839067459106f, -0.33280691504478455f,
+                                           0.1286155879497528f, -0.037672240287065506f}}
+                         : TanhFit{0.45f, {1.f, -0.3332953155040741f, 0.1323312669992447f,
+                                           -0.04587532579898834f}};
+}
 
 // What a score goes through: nothing (every row of a tile sees the same keys), a key range per
 // row, or that and a cap, a distance bias or both (instances of their own: what the others need
@@ -158,6 +168,7 @@ struct Args {
   int num_seqs, num_tokens, max_blocks, q_heads, kv_heads, group, num_blocks;
   float scale;                  // (* k_scale of an E4M3 cache)
   float cap;                    // 0: none
+  TanhFit fit;                  // of the cap
   float v_scale;
   const float *k_scales, *v_scales;  // [Hkv] or null
   int ctas;                     // most runs
@@ -687,7 +698,7 @@ __global__ void __launch_bounds__(threads(F8), 2)
       // Scores in base 2: with a cap c, x -> c log2(e) tanh(x / c); the bias is taken relative
       // to the row's nearest key, so that it is exact where weights are (the softmax does not
       // change): -slope (|p - t| - nearest).
-      float in = sl, amp = 0.f, slope = 0.f, near = 0.f, curve = kNearTanh;
+      float in = sl, amp = 0.f, slope = 0.f, near = 0.f, curve = 0.f;
       float w0 = 0.f, w1 = 0.f, w2 = 0.f, w3 = 0.f;
       if constexpr (kChanged) {
         if constexpr (kCap) {
@@ -698,8 +709,8 @@ __global__ void __launch_bounds__(threads(F8), 2)
           w0 = amp * by, w1 = w0 * by2, w2 = w1 * by2, w3 = w2 * by2;
           // powers that fp32 does not hold, or only as infinity, which times a score of zero is NaN:
           // the other form
-          if (by < 0x1p-12f || !(w3 <= 0x1p100f)) curve = -1.f;
-          w0 *= kTanh0, w1 *= kTanh1, w2 *= kTanh2, w3 *= kTanh3;
+          curve = w3 >= 0x1p-100f && w3 <= 0x1p100f ? a.fit.near : -1.f;
+          w0 *= a.fit.c[0], w1 *= a.fit.c[1], w2 *= a.fit.c[2], w3 *= a.fit.c[3];
         }
         if constexpr (kBias) {
           slope = a.slopes[head] * 1.4426950408889634f;
@@ -768,7 +779,7 @@ __global__ void __launch_bounds__(threads(F8), 2)
                 f1 = max3(f1, fabsf(__uint_as_float(x[c + 2])), fabsf(__uint_as_float(x[c + 3])));
               }
               if (!__any_sync(kFullMask, fmaxf(f0, f1) * in > curve)) {
-                // y P(y^2), P of degree 3 fitted to tanh(y) / y: off by 2^-19.7 up to there.
+                // y P(y^2), P of degree 3 fitted to tanh(y) / y.
                 // Five multiply-adds of two scores each, two cycles each, where the other form
                 // takes twelve a score for its special functions
                 const uint64_t q0 = f32x2(w0, w0), q1 = f32x2(w1, w1), q2 = f32x2(w2, w2);

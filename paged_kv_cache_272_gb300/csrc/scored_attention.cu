@@ -192,7 +192,8 @@ int scored_impl(uint16_t *out, const uint16_t *q, const void *k_cache, const voi
   carve(a, ws, workspace, head_dim);
   a.out = out, a.q = q, a.k_cache = k_cache, a.v_cache = v_cache;
   a.block_tables = block_tables, a.context_lens = context_lens, a.starts = query_start;
-  a.key_begin = key_begin, a.key_end = key_end, a.slopes = slopes, a.cap = cap;
+  a.key_begin = key_begin, a.key_end = key_end, a.slopes = slopes;
+  a.cap = cap, a.fit = tanh_fit(cap);
   a.num_seqs = num_seqs, a.num_tokens = num_tokens, a.max_blocks = max_blocks_per_seq;
   a.q_heads = num_q_heads, a.kv_heads = num_kv_heads, a.num_blocks = num_blocks;
   a.scale = (float)((double)scale * (double)k_scale);

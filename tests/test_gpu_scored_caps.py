@@ -40,3 +40,42 @@ def test_scores_of_zero(ops, cap, D, f8):
         for t in range(64):
             w.k[int(w.bt[0, t // 16]), :, t % 16] = 0
         check(ops, w, "keys")
+
+
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cap", [128.0, 1000.0, 4096.0])
+def test_large_caps_within_the_bound_of_all(ops, cap, D, f8):
+    """Scores to about 35, far below the cap: off by 2^-23.6 of the cap at most (at 4096 3.2e-4), and by
+    the products' rounding (128 of magnitude 16 at 2^-24 each, 1.2e-4): a weight moves by less than
+    2^-11 of itself, the result by twice that, within the 2^-10 of every other case."""
+    w = Scored([(300, 9), (700, 1)], 8, 2, D, "causal", cap=cap, seed=25, f8=f8)
+    w.q *= 4
+    check(ops, w)
+
+
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("part", [0.1, 0.16, 0.32, 0.44])
+@pytest.mark.parametrize("cap", [64.0, 65.0, 4096.0])
+def test_tiles_of_both_forms(ops, cap, part, f8):
+    """Equal scores in two tiles, one of which holds a far score of the other sign: the two forms of
+    the tanh agree, so that V of 1 and of -1 cancel.  Each is within 2^-21 of the cap (at 4096 0.002;
+    their difference of 0.0013, as their sources add up: 2^-23.6 and 1.2 2^-22, moves the result by half
+    of that, below the bound's 2^-10)."""
+    w = Scored([(128, 1)], 2, 1, 64, "causal", cap=cap, seed=26, f8=f8)
+    w.q[:] = 1
+    b = torch.as_tensor(w.bt[0]).long()
+    x = part * cap          # the score of all keys but one, whose score is -16 x
+    v = torch.where(torch.arange(128) < 64, 1.0, -1.0).view(8, 16)
+    if f8:
+        code = lambda t: t.to(torch.float8_e4m3fn).view(torch.uint8)
+        w.ks[:], w.vs[:] = x / 8, 1.0
+        k = torch.ones(8, 1, 16, 64)
+        k[5, 0, 3] = -16
+        w.k[b], w.v.view(w.NB, 1, 64, 16)[b] = code(k), code(v.view(8, 1, 1, 16).expand(8, 1, 64, 16))
+    else:
+        k = torch.full((8, 1, 16, 64), x / 8)
+        k[5, 0, 3] = -2 * x
+        w.k[b] = k.to(torch.bfloat16)
+        w.v[b] = v.view(8, 1, 16, 1).expand(8, 1, 16, 64).to(torch.bfloat16)
+    check(ops, w, (cap, part))
