@@ -22,7 +22,7 @@ namespace {
 // in groups of 4 42, 36; 114 MB 34, 34; E4M3 57 MB 38, 32; 114 MB 40, 38; 195 MB 56, 60).
 constexpr int kLeastTiles = 16, kLeastBytes = 100 << 20;
 // Own keys are cut into records of half of a CTA's share, of at least 256 tokens.
-constexpr int kOwnPerCta = 2, kLeastOwn = 256;
+constexpr int kOwnPerCta = 2, kLeastOwn = 256, kMostOwn = INT_MAX & ~31;
 
 // The prefixes' K and V from which on a group's row tiles run side by side, in lanes: with less, L2
 // keeps the keys from one row tile's read to the next.
@@ -231,8 +231,9 @@ __device__ __forceinline__ void plan_own(const Args &a, const OwnArgs &own, cons
   // The size of a record, then the records, longest first (by 32nds of that size).
   const unsigned long long share =
       quotient(tokens * (unsigned)own.per_token, (unsigned)kOwnPerCta * (unsigned)own.slots);
+  // (the most that an int holds: above, no sequence has more than one record)
   const int P = (int)(share < kLeastOwn ? (unsigned long long)kLeastOwn
-                                        : min((share + 32) & ~31ull, 1ull << 30));
+                                        : min((share + 32) & ~31ull, (unsigned long long)kMostOwn));
   auto bin_of = [&](int len) {  // of a record that is not whole
     return kBins - (int)quotient((unsigned long long)len * kBins + P - 1, (unsigned)P);
   };
@@ -272,7 +273,8 @@ __device__ __forceinline__ void plan_own(const Args &a, const OwnArgs &own, cons
     if (s < s1) {
       SeqParts o = {s + (int)(more + ex), parts, 0, -1};
       if (k.from > 0) o.index = s - gr.starts[k.group], o.prefix = gr.tile0[k.group];
-      // P keeps this so for any tables that memory holds
+      // P keeps this so: there are at most tokens / P records besides a sequence's first, for which
+      // the capacity has 2 slots / per_token (and none where P is kMostOwn)
       const bool fits = (int64_t)o.own + parts <= own.capacity;
       if (!fits) {
         flag_error(a.err, PKV_DEV_BAD_CONTEXT);
