@@ -36,7 +36,7 @@
 //
 // What bounds it (GB300): a decode of 24 sequences of up to 8192 keys, 32 heads, reads its 2.16 GB at
 // 6.6 TB/s, the copy's rate.  Chunks of 512 (eight, window 4096, 32 heads on 8) are bound by the
-// softmax warps, two a scheduler: 259 us, 1060 TFLOP/s; 354 with a cap (no pipe above 36%, 2.1 issues
+// softmax warps, two a scheduler: 259 us, 1060 TFLOP/s; 357 with a cap (no pipe above 36%, 2.1 issues
 // a cycle and SM).  Short ranges (packed documents, 7 key tiles a segment: 55 us)
 // by a segment's start and finish, the plan and the join.
 #pragma once
@@ -1386,8 +1386,8 @@ int launch(Args a, cudaStream_t st) {
       (!F8 && !kv_tensor_map(&tv, a.v_cache, rows, D, 2)))
     return PKV_ERR_CUDA;
   // Shared prefixes: the two launches behind read the plan without waiting for this one, so the
-  // plan is complete before this one starts.  (Chats 65 us a call, 62 in a graph, as with a dependent
-  // launch; its calls one by one took 64.  With both launches waiting: 73, and 71 in a graph.)
+  // plan is complete before this one starts.  (In a graph as fast as a dependent launch, calls one
+  // by one 1 to 4 us slower; with both launches waiting chats take 9 us more, documents 18.)
   const auto kernel = range_attention_kernel<D, F8, MODE>;
   const dim3 grid((unsigned)a.ctas), block(threads(F8));
   const size_t smem = Lay::kSmemLaunch;

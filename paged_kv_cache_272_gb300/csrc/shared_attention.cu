@@ -7,8 +7,8 @@
 // range_attention.cuh's kernel have all their rows.  A sequence alone has 8 of 128; its own keys
 // go through the decode kernel's mma.sync tiles of 8 rows (attention_mma.cu), which read short key
 // ranges at memory speed where a row tile's start and finish would take as long as their keys
-// (long documents: 190 us, 263 with row tiles for all keys; E4M3, head_dim 64: 61, 149; chats under
-// one prompt: 65, 62).
+// (long documents: 189 us, 263 with row tiles for all keys; E4M3, head_dim 64: 63, 149; for chats under
+// one prompt row tiles for all were faster: 68, 62).
 #include "attention.cuh"
 #include "range_attention.cuh"
 
@@ -24,9 +24,13 @@ constexpr int kLeastTiles = 16, kLeastBytes = 100 << 20;
 // Own keys are cut into records of half of a CTA's share, of at least 256 tokens.
 constexpr int kOwnPerCta = 2, kLeastOwn = 256, kMostOwn = INT_MAX & ~31;
 
-// The prefixes' K and V from which on a group's row tiles run side by side, in lanes: with less, L2
-// keeps the keys from one row tile's read to the next.
-// (34 MB: 71 us in lanes, 75 not; 0.7 GB: 194, 251; 4 row tiles of 490 MB: 175, 267.)
+// The prefixes' K and V from which on a group's row tiles run side by side, in lanes: their keys
+// come from DRAM once, where L2 does not hold them all; with few keys lanes cut the pairs into more
+// segments than runs laid end to end do.  (bf16, us in lanes and not, one group of 4 row tiles, two of
+// 2, four of 2: 8 MB 43.0 and 42.6, 35.4 and 29.1, 48.7 and 45.9; 16 MB 44.9 and 46.8, 43.2 and 42.9,
+// 52.0 and 53.1; 24 MB 50.1 and 51.0, 44.4 and 45.7, 54.4 and 55.9; 96 MB 74.5 and 76.3, 61.3 and 62.4,
+// 71.5 and 72.5; 0.7 GB 194 and 251; 4 row tiles of 490 MB 175 and 267.  E4M3 from 8 to 96 MB
+// within 4% of each other.)
 constexpr int kLaneBytes = 24 << 20;
 // Rows up to which the join takes a CTA for each (512 rows of 20 parts: 34 us so, 36 with a warp a
 // row; 2048: 40 and 34).

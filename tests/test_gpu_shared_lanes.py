@@ -1,5 +1,5 @@
-"""Shared prefixes whose keys are too many for L2 to keep between a group's row tiles: these run side
-by side, in lanes of their own, and a pair of row tile and head is cut over runs that lie apart."""
+"""Shared prefixes of 24 MB and more: a group's row tiles run side by side, in lanes of their own, and a
+pair of row tile and head is cut over runs that lie apart."""
 import numpy as np
 import pytest
 import torch
